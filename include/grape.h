@@ -389,6 +389,107 @@ GRAPE_API int grape_layer_sqnorms_static(const void* A, const void* Gout, int32_
                                          uint32_t layer, uint32_t step, float* sqnorms_out,
                                          void* stream);
 
+/* ---- the two ends of a language model around the stack of linear layers ---------------
+ *
+ * Token embedding (its output is the first A), a vocabulary head with its loss and
+ * distillation from a teacher's logits (their gradients are Gout), and the embedding
+ * table's gradient in the per-sample form that the method needs.  A gradient of a table is
+ * a sum over tokens like a linear layer's, and clipping takes a sample's norm over all its
+ * parameters before the sum ("Metodologia: DP-GRAPE", design choice 2, technical summary of
+ * "Memory-Efficient Differentially Private Training with Gradient Random Projection"); the
+ * pages have no formula for either end, so each call states its own.
+ *
+ * None of these calls needs a context: each works on the current device, enqueues on
+ * `stream`, allocates and synchronises nothing (so it may be captured into a CUDA graph)
+ * and keeps no state between calls.  Scratch is the caller's: a call's workspace may be
+ * reused as soon as the call's work is done, and two calls whose work may overlap need one
+ * each.  Device pointers of matrices, workspaces and outputs are 16-byte aligned; ids,
+ * weights and per-row vectors need the alignment of their elements.  Token numbers (ids, labels, teacher
+ * indices) are int32 or int64: id_bytes is 4 or 8.  A number outside [0, vocab) is no error:
+ * it means "no token" as each call states.  Errors are reported through
+ * grape_global_error(): GRAPE_EINVAL (arguments), GRAPE_EUNSUPPORTED (not an sm_100a device,
+ * or no tensor-map encoder in the driver), GRAPE_ECUDA. */
+
+/* out[n] = scale * table[ids[n]] for n < n_ids: the lookup with scaling.
+ *  table      vocab x d, table_dtype (GRAPE_F32 or GRAPE_BF16)
+ *  out        n_ids x d, out_dtype; computed in fp32 and rounded once.  A row whose id lies outside
+ *             [0, vocab) (padding) is zero. */
+GRAPE_API int grape_embed(const void* table, int32_t table_dtype, const void* ids, int32_t id_bytes,
+                          int64_t n_ids, int32_t vocab, int32_t d, double scale, int32_t out_dtype,
+                          void* out, void* stream);
+
+/* The tokens of a batch sorted by (token, position), which both reductions below read: one
+ * order serves a batch's norms and its gradient.  `order` is a caller-owned device buffer of
+ * grape_embed_order_bytes bytes.  It starts with n_ids int32 positions in sorted order
+ * (positions of ids outside [0, vocab) last, themselves in order) and, at the next multiple of 256
+ * bytes, their n_ids int32 tokens (vocab for those); the rest is private.  n_ids <= 2^30. */
+GRAPE_API int grape_embed_order_bytes(int64_t n_ids, int32_t vocab, uint64_t* bytes);
+GRAPE_API int grape_embed_order(const void* ids, int32_t id_bytes, int64_t n_ids, int32_t vocab,
+                                void* order, void* stream);
+
+/* Bytes of the workspace of grape_embed_sqnorms and grape_embed_grad. */
+GRAPE_API int grape_embed_workspace_bytes(int32_t B, int32_t T, int32_t vocab, int32_t d, uint64_t* bytes);
+
+/* sqnorms[i] = || G_i ||_F^2 (B floats), where G_i[v] = scale * sum over sample i's tokens
+ * t with id v of Gout[i][t]: the squared norm of sample i's gradient of the table, to be
+ * added to grape_sqnorms' before clipping.  Repeated tokens of a sample are summed before the
+ * square.
+ *  order      of the batch's B*T ids (row-major B x T)
+ *  Gout       B x T x d, dtype: the loss gradient with respect to grape_embed's output */
+GRAPE_API int grape_embed_sqnorms(const void* order, int32_t B, int32_t T, int32_t vocab, int32_t d,
+                                  const void* Gout, int32_t dtype, double scale, void* workspace,
+                                  float* sqnorms, void* stream);
+
+/* grad = sum_i weights[i] G_i, with G_i as above: vocab x d fp32, every row written (zero
+ * where no token fell).  weights: B floats (the clip factors c_i), NULL for 1.  Sums are
+ * fp32 in a fixed order: the same inputs give the same bits. */
+GRAPE_API int grape_embed_grad(const void* order, int32_t B, int32_t T, int32_t vocab, int32_t d,
+                               const void* Gout, int32_t dtype, double scale, const float* weights,
+                               void* workspace, float* grad, void* stream);
+
+/* Softmax cross entropy of a vocabulary head, forward and backward, without keeping the logits
+ * z[n][v] = H[n] . W[v]: they are formed in pieces of the vocabulary and reduced at once.
+ *   loss[n]  = weights[n] * (log sum_v exp z[n][v] - z[n][labels[n]])
+ *   dH[n]    = weights[n] * sum_v (p[n][v] - [v = labels[n]]) W[v]
+ *   dW[v]    = sum_n weights[n] * (p[n][v] - [v = labels[n]]) H[n]
+ *  H          N x d, W  vocab x d (a row per token, as the embedding table), dtype
+ *  labels     N token numbers; a row whose label lies outside [0, vocab), or whose weight is 0, has
+ *             no loss: its loss and dH are 0, and its H is not read (it may hold NaN)
+ *  weights    N floats (a token's share of its sample's loss, a clip factor), NULL for 1
+ *  loss       N floats
+ *  dH, dW     N x d and vocab x d in dtype, or NULL: not computed
+ *  workspace  grape_head_loss_bytes bytes: the live rows of H, 8 N vocab / 128 bytes of partial
+ *             sums, one piece of the logits' gradient (at most 128 MiB, or 4096 columns for a
+ *             large N), for fp32 or d % 8 != 0 a laid-out copy of W, and fp32 sums of dH where it
+ *             is summed in pieces
+ * All sums are fp32; with bf16 inputs the logits' gradient is rounded to bf16 before the second
+ * products, with fp32 inputs products keep 24 bits.  If a bounded device-side wait gives up,
+ * every loss is NaN.  N <= 2^30, N * vocab / 65536 < 2^31. */
+GRAPE_API int grape_head_loss_bytes(int64_t N, int32_t d, int32_t vocab, int32_t dtype, int32_t want_dH,
+                                    int32_t want_dW, uint64_t* bytes);
+GRAPE_API int grape_head_loss(const void* H, const void* W, const void* labels, int32_t id_bytes,
+                              const float* weights, int64_t N, int32_t d, int32_t vocab, int32_t dtype,
+                              void* workspace, float* loss, void* dH, void* dW, void* stream);
+
+/* Distillation from a teacher's top logits, forward and backward in one pass.  With p[n] =
+ * softmax(logits[n] / temperature) over the vocabulary and q[n] the softmax of
+ * values[n] / temperature over the row's valid entries (indices inside [0, vocab)):
+ *   loss[n]    = weights[n] * temperature^2 * sum_k q[n][k] (log q[n][k] - log p[n][index k])
+ *   Gout[n][v] = weights[n] * temperature * (p[n][v] - sum of q[n][k] with index k = v)
+ * Gout is the gradient with respect to the logits: Gout of a head that is a layer of the stack.
+ * One entry of any value is a hard label.  An index that occurs twice counts with both masses.
+ *  logits     N x vocab, dtype
+ *  indices    N x K token numbers, values N x K in value_dtype (1 <= K <= 1024)
+ *  weights    N floats, NULL for 1.  A row with weight 0 or without a valid entry has loss 0 and
+ *             Gout 0, whatever its logits hold.
+ *  Gout       N x vocab, dtype; may be `logits` itself (overwritten in place) and must not
+ *             overlap it otherwise
+ * Statistics are fp32, Gout is rounded once.  N <= 2^31 - 1, temperature > 0. */
+GRAPE_API int grape_distill_loss(const void* logits, int32_t dtype, int64_t N, int32_t vocab,
+                                 const void* indices, int32_t id_bytes, const void* values,
+                                 int32_t value_dtype, int32_t K, const float* weights, double temperature,
+                                 float* loss, void* Gout, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -4,4 +4,5 @@
 in-tree with ``python -m random_gradient_projection_b200.build``.
 """
 from . import grape  # noqa: F401
+from . import lm  # noqa: F401
 from .grape import GrapeStep, GrapeError  # noqa: F401

@@ -14,6 +14,7 @@
 #include "../../include/grape.h"
 #include "compact.h"
 #include "kernels.h"
+#include "lm.h"
 #include "tc.h"
 
 namespace {
@@ -44,6 +45,9 @@ int fault_alloc_index() {
 }
 
 }  // namespace
+
+// The reason of a failed call without a context, for the entry points of other files.
+int grape::fail_global(int code, const std::string& msg) { return set_global(code, msg); }
 
 struct grape_ctx {
   grape::StepShape sh{};

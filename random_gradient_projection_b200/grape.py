@@ -35,6 +35,9 @@ EXPORTS = (
     "grape_enable_compaction", "grape_step_masked", "grape_live_counts", "grape_set_norm_method",
     "grape_set_graph", "grape_selftest_wait_timeout", "grape_S_all", "grape_context_bytes",
     "grape_set_aggregation", "grape_aggregation_of",
+    "grape_embed", "grape_embed_order_bytes", "grape_embed_order", "grape_embed_workspace_bytes",
+    "grape_embed_sqnorms", "grape_embed_grad", "grape_head_loss_bytes", "grape_head_loss",
+    "grape_distill_loss",
 )
 GRAPE_NORM_DIRECT, GRAPE_NORM_GHOST = 0, 1
 GRAPE_AGG_AUTO, GRAPE_AGG_RECOMPUTE, GRAPE_AGG_STORE = 0, 1, 2
@@ -62,7 +65,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         raise ImportError(f"{path} is missing: build it with `python -m random_gradient_projection_b200.build`")
     lib = ctypes.CDLL(path)
     vp, i32, i64, u32, u64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32, ctypes.c_uint64
-    pp = ctypes.POINTER(ctypes.c_void_p)
+    pp, f64 = ctypes.POINTER(ctypes.c_void_p), ctypes.c_double
     sig = {
         "grape_create": ([ctypes.POINTER(grape_layer), i32, i32, ctypes.c_double, ctypes.c_double, u64,
                           ctypes.POINTER(grape_adam), i32, i32, i32, i32, ctypes.POINTER(vp)], i32),
@@ -98,6 +101,15 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "grape_S_all": ([vp, ctypes.POINTER(vp), ctypes.POINTER(i64)], i32),
         "grape_set_aggregation": ([vp, i32], i32),
         "grape_aggregation_of": ([vp, ctypes.POINTER(i32)], i32),
+        "grape_embed": ([vp, i32, vp, i32, i64, i32, i32, f64, i32, vp, vp], i32),
+        "grape_embed_order_bytes": ([i64, i32, ctypes.POINTER(u64)], i32),
+        "grape_embed_order": ([vp, i32, i64, i32, vp, vp], i32),
+        "grape_embed_workspace_bytes": ([i32, i32, i32, i32, ctypes.POINTER(u64)], i32),
+        "grape_embed_sqnorms": ([vp, i32, i32, i32, i32, vp, i32, f64, vp, vp, vp], i32),
+        "grape_embed_grad": ([vp, i32, i32, i32, i32, vp, i32, f64, vp, vp, vp, vp], i32),
+        "grape_head_loss_bytes": ([i64, i32, i32, i32, i32, i32, ctypes.POINTER(u64)], i32),
+        "grape_head_loss": ([vp, vp, vp, i32, vp, i64, i32, i32, i32, vp, vp, vp, vp, vp], i32),
+        "grape_distill_loss": ([vp, i32, i64, i32, vp, i32, vp, i32, i32, vp, f64, vp, vp, vp], i32),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -315,6 +327,59 @@ def grape_philox_words(seed: int, layer: int, step: int, stream_id: int, n_block
 def grape_gaussian(seed: int, layer: int, step: int, stream_id: int, n: int, out, stream=None):
     _check(lib().grape_gaussian(seed & (2**64 - 1), layer, step, stream_id, n, _ptr(out),
                                 _stream(stream)))
+
+
+def grape_embed(table, table_dtype: int, ids, id_bytes: int, n_ids: int, vocab: int, d: int, scale: float,
+                out_dtype: int, out, stream=None):
+    _check(lib().grape_embed(_ptr(table), table_dtype, _ptr(ids), id_bytes, n_ids, vocab, d, scale,
+                             out_dtype, _ptr(out), _stream(stream)))
+
+
+def grape_embed_order_bytes(n_ids: int, vocab: int) -> int:
+    out = ctypes.c_uint64()
+    _check(lib().grape_embed_order_bytes(n_ids, vocab, ctypes.byref(out)))
+    return out.value
+
+
+def grape_embed_order(ids, id_bytes: int, n_ids: int, vocab: int, order, stream=None):
+    _check(lib().grape_embed_order(_ptr(ids), id_bytes, n_ids, vocab, _ptr(order), _stream(stream)))
+
+
+def grape_embed_workspace_bytes(B: int, T: int, vocab: int, d: int) -> int:
+    out = ctypes.c_uint64()
+    _check(lib().grape_embed_workspace_bytes(B, T, vocab, d, ctypes.byref(out)))
+    return out.value
+
+
+def grape_embed_sqnorms(order, B: int, T: int, vocab: int, d: int, Gout, dtype: int, scale: float, workspace,
+                        sqnorms, stream=None):
+    _check(lib().grape_embed_sqnorms(_ptr(order), B, T, vocab, d, _ptr(Gout), dtype, scale, _ptr(workspace),
+                                     _ptr(sqnorms), _stream(stream)))
+
+
+def grape_embed_grad(order, B: int, T: int, vocab: int, d: int, Gout, dtype: int, scale: float, weights,
+                     workspace, grad, stream=None):
+    _check(lib().grape_embed_grad(_ptr(order), B, T, vocab, d, _ptr(Gout), dtype, scale, _ptr(weights),
+                                  _ptr(workspace), _ptr(grad), _stream(stream)))
+
+
+def grape_head_loss_bytes(N: int, d: int, vocab: int, dtype: int, want_dH: bool, want_dW: bool) -> int:
+    out = ctypes.c_uint64()
+    _check(lib().grape_head_loss_bytes(N, d, vocab, dtype, int(want_dH), int(want_dW), ctypes.byref(out)))
+    return out.value
+
+
+def grape_head_loss(H, W, labels, id_bytes: int, weights, N: int, d: int, vocab: int, dtype: int, workspace,
+                    loss, dH=None, dW=None, stream=None):
+    _check(lib().grape_head_loss(_ptr(H), _ptr(W), _ptr(labels), id_bytes, _ptr(weights), N, d, vocab, dtype,
+                                 _ptr(workspace), _ptr(loss), _ptr(dH), _ptr(dW), _stream(stream)))
+
+
+def grape_distill_loss(logits, dtype: int, N: int, vocab: int, indices, id_bytes: int, values, value_dtype: int,
+                       K: int, weights, temperature: float, loss, Gout, stream=None):
+    _check(lib().grape_distill_loss(_ptr(logits), dtype, N, vocab, _ptr(indices), id_bytes, _ptr(values),
+                                    value_dtype, K, _ptr(weights), temperature, _ptr(loss), _ptr(Gout),
+                                    _stream(stream)))
 
 
 # ---- buffer checks of the context owner below ---------------------------------
