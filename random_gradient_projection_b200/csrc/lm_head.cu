@@ -5,34 +5,51 @@
 //   g_nv = w_n (exp(z_nv - lse_n) - [v = label_n])
 //   dH_n = sum_v g_nv W_v,   dW_v = sum_n g_nv h_n
 //
-// Four contractions on one warp-specialised kernel, head_gemm_kernel<EPI, PLANES>:
+// The contractions run on one warp-specialised kernel, head_gemm_kernel<EPI, PLANES>:
 //
 //   STATS  z over the whole vocabulary, reduced in the epilogue to a maximum and a sum of
-//          exponentials per row and 128 columns (and the label's logit)
-//   GRAD   z again for one piece of the vocabulary; the epilogue writes g (bf16) for the piece
-//   DH     dH (+)= g W over the piece          (K = the piece's columns, split when rows are few)
+//          exponentials per row and tile (and the label's logit)
+//   GRAD   z again for one piece of the vocabulary; the epilogue writes g for the piece
+//   EXP    z once for one piece; the epilogue writes e_nv = exp(z_nv - r_n) and its row sums,
+//          with a reference r_n that is known beforehand
+//   DH     dH (+)= g W, or e W, over the piece (K = the piece's columns, split when rows are few)
 //   DW     dW of the piece = g^T H             (K = rows)
 //
-// so the memory is one piece of g, at most kPieceBytes (or 4096 columns), whatever V is.  The price
-// is the second product z: 6 (8) N V d flops for dH (and dW) where keeping the logits takes 4 (6).
+// so the memory is one piece of g (at most kPieceBytes, or 4096 columns), whatever V is.
 //
-// Rows without a loss (label outside [0, V), or weight 0) are dropped first: the live rows are
-// gathered in order into a compact H, so masked rows cost nothing, and whatever they hold (NaN
-// included) reaches no sum.  The number of live rows is known on the device only; every kernel
-// reads it there.
+// With dW, or for a small problem, STATS comes first and GRAD recomputes z: 6 (8) N V d flops for
+// dH (and dW), where keeping the logits takes 4 (6).  With dH alone the recomputation is not needed:
+// softmax times W can be summed before the softmax is normalised,
 //
-// Precision.  bf16 inputs: products are exact in the tensor core and accumulate in fp32; g is
+//   dH_n = w_n (sum_{v != label} e_nv W_v / s_n - (1 - p_n) W_label),   s_n = sum_v e_nv,
+//
+// and the label's own logit, one short dot product per row, is a reference r_n that keeps every
+// e_nv at most exp(l_n) and s_n at least 1.  So EXP overflows only where a row's loss passes 60;
+// an epilogue that sees this sets `retry`, and the two-pass kernels, which are launched behind
+// and otherwise leave at once, compute the call anew.  (The label's column is left out of e and of
+// the sum, so that 1 - p_n = s'_n / s_n and l_n = log1p(s'_n / e_label) stay exact for p_n near 1.)
+//
+// Rows without a loss (label outside [0, V), or weight 0) are dropped first: where there are any,
+// the live rows are gathered in order into a compact H, so masked rows cost nothing, and whatever
+// they hold (NaN included) reaches no sum.  The number of live rows is known on the device only;
+// every kernel reads it there.
+//
+// Precision.  bf16 inputs: products are exact in the tensor core and accumulate in fp32; g (or e) is
 // rounded once to bf16 as the operand of the second product (relative 2^-8 at most per element,
 // independent from element to element, so it averages out in the sums), as the method's own
 // step does with AP.  fp32 inputs (PLANES = 3): each operand is split into three bf16 planes
 // x = x0 + x1 + x2 (24 bits together) and the six products of order up to 2^-16 are accumulated,
 // smallest first; the three dropped ones are below 2^-24 relative.  Six tensor-core products
-// run several times faster than one on the fp32 cores.
+// run several times faster than one on the fp32 cores.  The tensor core's accumulator truncates at
+// every step (measured: logits of one sign come out low by 1.7e-8 per step of K = 16, 4.2e-6 at
+// d = 4096), so sums that end in an fp32 result leave TMEM every kChunk blocks and are added,
+// rounded to nearest, in registers.
 //
 // The kernel: a cluster of two CTAs (one tile of 256 x 256, cta_group::2), each CTA with half of
-// A's rows and half of B's columns in its ring of shared-memory stages.  Warps 0 and 10-12 of each
-// CTA load by TMA, warp 1 of CTA 0 issues the MMAs for both, warps 2-9 are the epilogue of their
-// CTA's 128 rows; two 256-column accumulators in TMEM let it overlap the next tile.
+// A's rows and half of B's columns in its ring of shared-memory stages.  Warps 17-19 of each
+// CTA load by TMA, warp 16 of CTA 0 issues the MMAs for both, warps 0-15 are the epilogue of their
+// CTA's 128 rows (each 32 rows x 64 columns, in registers); two 256-column accumulators in TMEM
+// let it overlap the next sums.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -54,35 +71,53 @@ constexpr int kHalf = 128;            // of a CTA
 constexpr int kBK = 64;
 constexpr int kStages = 6;
 constexpr int kStage = 2 * kHalf * kBK * 2;   // A half and B half: 32 KB
-constexpr int kEpiWarps = 8;
-constexpr int kProducers = 4;
-constexpr int kThreads = 32 * (2 + kEpiWarps + kProducers - 1);
-constexpr int kBox = 32 * 128;        // an epilogue warp's staging box: 32 rows x 128 bytes
+constexpr int kEpiWarps = 16;
+constexpr int kCols = 64;             // columns of an epilogue warp
+constexpr int kMmaWarp = kEpiWarps;   // then the producers: together a fifth warpgroup
+constexpr int kProducers = 3;
+constexpr int kThreads = 32 * (kEpiWarps + 1 + kProducers);
+// Registers per thread: 640 threads are launched with 96 each (61440); the epilogue's 512 take
+// 112, the other 128 keep 32 (61440 again; without this the epilogues spill).
+constexpr int kRegsLaunch = 96, kRegsEpi = 112, kRegsOther = 32;
+static_assert(kThreads == 640 && 512 * kRegsEpi + 128 * kRegsOther <= kThreads * kRegsLaunch, "register split");
+constexpr int kBox = 32 * 64;         // an epilogue warp's staging box: 32 rows x 64 bytes
 constexpr int kBarOff = kStages * kStage;
 constexpr int kBoxOff = kBarOff + 1024;
 constexpr int kSmem = kBoxOff + kEpiWarps * kBox + 1024;   // + alignment slack
+static_assert(kBoxOff % 1024 == 0, "boxes are aligned");
 static_assert(kProducers <= kStages, "parity waits need at most as many producers as stages");
 static_assert(kSmem <= 227 * 1024, "shared memory of an SM");
 constexpr int kGroupM = 8;            // row tiles that share a column of B tiles in L2
 constexpr uint64_t kWaitLimitNs = 4000000000ull;
 constexpr uint64_t kDrainNs = 20000000ull;
-constexpr size_t kPieceBytes = size_t(128) << 20;
+constexpr size_t kPieceBytes = size_t(256) << 20;
+constexpr float kExpLimit = 1e26f;     // exp(60): sums of 2^17 such terms, times W, stay in fp32
 constexpr int kErrTimeout = 1;
 #ifdef GRAPE_CHECKED
 constexpr int kErrBounds = 8;   // a TMA box off the 16-byte rule or at a negative coordinate (skipped)
 #endif
 
-enum Epi : int { STATS = 0, GRAD = 1, DH = 2, DW = 3 };
+enum Epi : int { STATS = 0, GRAD = 1, EXP = 2, DH = 3, DW = 4 };
+
+// Blocks of 64 that stay in the tensor core's accumulator at most.
+template <int EPI, int PLANES>
+struct Chunk {
+  static constexpr int kBlocks = PLANES == 3 ? 8 : (EPI == STATS || EPI == EXP) ? 16 : 1 << 30;
+};
 
 // Device words at the start of the workspace.
 struct HeadState {
   int err;
   int n_live;
+  int retry;   // EXP met a row whose loss is too large for its reference
 };
 
 struct HeadGemm {
   CUtensorMap mapA, mapB;
+  CUtensorMap mapH;     // H itself in place of its compact copy, when every row is live
+  int direct;           // mapH may be used: 1 for A, 2 for B
   HeadState* state;
+  int only_retry;       // leave at once unless state->retry
   int m_tiles;          // DW: vocabulary tiles of the piece; otherwise from n_live
   int n_tiles, splits;  // column tiles; parts of the K extent (DH)
   int kblocks;          // K extent in blocks of 64 (DW: from n_live)
@@ -91,15 +126,18 @@ struct HeadGemm {
   int64_t n_pad;        // rows of the compact buffers
   const int* labels;    // compact rows
   const float* weights;
-  const float* lse;
-  float2* parts;        // STATS: [128-column slot][n_pad] (maximum, sum of exponentials)
-  float* target;        // STATS: the label's logit
-  __nv_bfloat16* g;     // GRAD: [n_pad][ldg]
+  const float* lse;     // GRAD
+  const float* ref;     // EXP: r_n
+  float2* parts;        // STATS: [tile][n_pad] (maximum, sum of exponentials); EXP: (sum, unused)
+  float* target;        // STATS: the label's logit; EXP: less r_n
+  __nv_bfloat16* g;     // GRAD, EXP: [n_pad][ldg]
   int64_t ldg;
-  int planeG;           // GRAD: elements from one plane of g to the next
+  int planeG;           // elements from one plane of g to the next
   float* acc;           // DH: [split][n_pad][ldacc] fp32 (several pieces or splits)
   int64_t ldacc;
   int add, last;        // DH: add to acc; write the result (no later piece, no splits)
+  const float2* coef;   // DH after EXP: w / s and w s' / s; null after GRAD
+  const void* W;        // DH after EXP: W as given, for the label's row
   const int* rows;      // compact row -> row of H
   void* out;            // dH or dW, dtype of H
   float* poison;        // loss: set to NaN if a wait gives up
@@ -153,11 +191,43 @@ __device__ __forceinline__ Tile tile_at(int t, int mt, int nt, int splits, int k
   return c;
 }
 
+__device__ __forceinline__ void epi_bar() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory"); }
+
+template <int PLANES>
+struct HeadType {
+  using T = __nv_bfloat16;
+};
+template <>
+struct HeadType<3> {
+  using T = float;
+};
+
+// Four consecutive results of a row, from column `col` on; those from d on do not exist.
+__device__ __forceinline__ void store4(float* o, const float (&x)[4], int col, int d) {
+  if (d % 4 == 0) {
+    *reinterpret_cast<float4*>(o) = make_float4(x[0], x[1], x[2], x[3]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (col + k < d) o[k] = x[k];
+  }
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* o, const float (&x)[4], int col, int d) {
+  if (d % 4 == 0) {
+    *reinterpret_cast<uint2*>(o) = make_uint2(pack2(x[0], x[1]), pack2(x[2], x[3]));
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (col + k < d) o[k] = __float2bfloat16_rn(x[k]);
+  }
+}
+
 template <int EPI, int PLANES>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     head_gemm_kernel(const __grid_constant__ HeadGemm p) {
   constexpr bool kAMn = EPI == DW, kBMn = EPI == DH || EPI == DW;
   constexpr int kProds = PLANES == 1 ? 1 : 6;
+  constexpr int kChunk = Chunk<EPI, PLANES>::kBlocks;
   constexpr uint32_t kIdesc = ptx::idesc_bf16(kTile, kTile, kAMn, kBMn);
 
   extern __shared__ uint8_t smem_raw[];
@@ -178,7 +248,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   };
 
   ptx::griddep_launch_dependents();
-  if (warp == 0 && lane == 0) {
+  if (p.only_retry) {
+    ptx::griddep_wait();
+    if (__ldcg(&p.state->retry) == 0) return;   // the same in every thread of the grid
+  }
+  if (threadIdx.x == 0) {
     *abort_flag = 0;
     for (int s = 0; s < kStages; ++s) {
       ptx::mbar_init(&full[s], 2);
@@ -192,7 +266,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     ptx::prefetch_tmap(&p.mapA);
     ptx::prefetch_tmap(&p.mapB);
   }
-  if (warp == 1) {
+  if (warp == kMmaWarp) {
     ptx::tmem_alloc_pair(tmem_slot, 512);
     ptx::tmem_relinquish_pair();
   }
@@ -209,15 +283,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int kblocks = EPI == DW ? (n_live + kBK - 1) / kBK : p.kblocks;
   const int tiles = mt * p.n_tiles * p.splits;
 
-  const int producer = warp == 0 ? 0 : (warp >= 2 + kEpiWarps ? warp - (1 + kEpiWarps) : -1);
-  if (producer >= 0) {
+  if (warp >= kMmaWarp) {
+    ptx::setmaxnreg_dec<kRegsOther>();   // the whole warpgroup, one instruction
+    if (warp > kMmaWarp) {
     // ---------------- TMA producers ----------------
+    const int producer = warp - kMmaWarp - 1;
     if (lane == 0) {
+      const bool all_live = n_live == p.n_rows;
+      const CUtensorMap* mapA = p.direct == 1 && all_live ? &p.mapH : &p.mapA;
+      const CUtensorMap* mapB = p.direct == 2 && all_live ? &p.mapH : &p.mapB;
       uint32_t it = 0;
       bool ok = true;
-      uint32_t full0[kStages];
-#pragma unroll
-      for (int s = 0; s < kStages; ++s) full0[s] = ptx::cluster_addr(&full[s], 0);
       for (int t = pair; ok && t < tiles; t += pairs) {
         const Tile c = tile_at(t, mt, p.n_tiles, p.splits, kblocks);
         const int am = c.m * kTile + static_cast<int>(rank) * kHalf;
@@ -248,17 +324,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #endif
             ptx::mbar_arrive_expect_tx_cluster(bar, kStage);
             if (kAMn) {
-              ptx::tma_load_2d_pair(sa, &p.mapA, bar, ax + am, k);
-              ptx::tma_load_2d_pair(sa + 8192, &p.mapA, bar, ax + am + 64, k);
+              ptx::tma_load_2d_pair(sa, mapA, bar, ax + am, k);
+              ptx::tma_load_2d_pair(sa + 8192, mapA, bar, ax + am + 64, k);
             } else {
-              ptx::tma_load_2d_pair(sa, &p.mapA, bar, ax + k, am);
+              ptx::tma_load_2d_pair(sa, mapA, bar, ax + k, am);
             }
             if (kBMn) {
               const int y = EPI == DH ? p.v0 + k : k;
-              ptx::tma_load_2d_pair(sb, &p.mapB, bar, bx + bn, y);
-              ptx::tma_load_2d_pair(sb + 8192, &p.mapB, bar, bx + bn + 64, y);
+              ptx::tma_load_2d_pair(sb, mapB, bar, bx + bn, y);
+              ptx::tma_load_2d_pair(sb + 8192, mapB, bar, bx + bn + 64, y);
             } else {
-              ptx::tma_load_2d_pair(sb, &p.mapB, bar, bx + k, p.v0 + bn);
+              ptx::tma_load_2d_pair(sb, mapB, bar, bx + k, p.v0 + bn);
             }
           }
         }
@@ -277,203 +353,266 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         while (ptx::globaltimer_ns() - t0 < kDrainNs) __nanosleep(1000);
       }
     }
-  } else if (warp == 1) {
+    } else {
     // ---------------- UMMA issuer (CTA 0) ----------------
     if (rank == 0 && lane == 0) {
-      uint32_t it = 0, tc = 0;
+      uint32_t it = 0, ch = 0;   // stage uses, accumulator uses
       bool ok = true;
-      for (int t = pair; ok && t < tiles; t += pairs, ++tc) {
+      for (int t = pair; ok && t < tiles; t += pairs) {
         const Tile c = tile_at(t, mt, p.n_tiles, p.splits, kblocks);
-        const int b = tc & 1;
-        const uint32_t use = tc >> 1;
-        if (use > 0 && !wait(&accempty[b], (use - 1) & 1)) {
-          fail(p, kErrTimeout);
-          break;
-        }
-        ptx::tc_fence_after();
-        const uint32_t dacc = tmem + b * kTile;
         const int steps = kProds * (c.kb1 - c.kb0);
-        for (int i = 0; i < steps; ++i, ++it) {
-          const int s = it % kStages;
-          if (!wait(&full[s], (it / kStages) & 1)) {
+        int i = 0;
+        do {
+          const int b = ch & 1;
+          const uint32_t use = ch >> 1;
+          if (use > 0 && !wait(&accempty[b], (use - 1) & 1)) {
             fail(p, kErrTimeout);
             ok = false;
             break;
           }
           ptx::tc_fence_after();
-          const uint32_t a_base = ptx::smem_u32(smem + s * kStage), b_base = a_base + kStage / 2;
+          const uint32_t dacc = tmem + b * kTile;
+          const int i0 = i, i1 = steps - i > kChunk ? i + kChunk : steps;
+          for (; i < i1; ++i, ++it) {
+            const int s = it % kStages;
+            if (!wait(&full[s], (it / kStages) & 1)) {
+              fail(p, kErrTimeout);
+              ok = false;
+              break;
+            }
+            ptx::tc_fence_after();
+            const uint32_t a_base = ptx::smem_u32(smem + s * kStage), b_base = a_base + kStage / 2;
 #pragma unroll
-          for (int k = 0; k < kBK / 16; ++k) {
-            const uint64_t ad = kAMn ? ptx::desc_sw128(a_base + k * 2048, 8192, 1024)
-                                     : ptx::desc_sw128(a_base + k * 32, 16, 1024);
-            const uint64_t bd = kBMn ? ptx::desc_sw128(b_base + k * 2048, 8192, 1024)
-                                     : ptx::desc_sw128(b_base + k * 32, 16, 1024);
-            ptx::umma_bf16_pair(dacc, ad, bd, kIdesc, (i > 0 || k > 0) ? 1u : 0u);
+            for (int k = 0; k < kBK / 16; ++k) {
+              const uint64_t ad = kAMn ? ptx::desc_sw128(a_base + k * 2048, 8192, 1024)
+                                       : ptx::desc_sw128(a_base + k * 32, 16, 1024);
+              const uint64_t bd = kBMn ? ptx::desc_sw128(b_base + k * 2048, 8192, 1024)
+                                       : ptx::desc_sw128(b_base + k * 32, 16, 1024);
+              ptx::umma_bf16_pair(dacc, ad, bd, kIdesc, (i > i0 || k > 0) ? 1u : 0u);
+            }
+            ptx::umma_commit_pair(&empty[s]);
           }
-          ptx::umma_commit_pair(&empty[s]);
-        }
-        ptx::umma_commit_pair(&accfull[b]);
+          ptx::umma_commit_pair(&accfull[b]);
+          ++ch;
+        } while (ok && i < steps);
       }
     }
+    }
   } else {
-    // ---------------- epilogue: warps 2..9 ----------------
-    const int ew = warp - 2, q = warp & 3, h = ew >> 2;
-    uint8_t* box = smem + kBoxOff + ew * kBox;
-    uint4* box4 = reinterpret_cast<uint4*>(box);
-    uint32_t tc = 0;
-    for (int t = pair; t < tiles; t += pairs, ++tc) {
+    // ---------------- epilogue: warps 0..15 ----------------
+    // Warp w: TMEM lanes 32 (w % 4).. (a hardware rule) and 64 of the tile's columns.
+    ptx::setmaxnreg_inc<kRegsEpi>();
+    const int q = warp & 3, h = warp >> 2;
+    uint8_t* box = smem + kBoxOff + warp * kBox;
+    // this lane's two values in the box of the warp with this lane quarter and columns h2
+    auto part_of = [&](int h2) {
+      return reinterpret_cast<float2*>(smem + kBoxOff + (4 * h2 + q) * kBox) + lane;
+    };
+    uint32_t ch = 0;
+    auto release = [&]() {   // this accumulator may be overwritten
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive_cluster(ptx::cluster_addr(&accempty[ch & 1], 0));
+      ++ch;
+    };
+    for (int t = pair; t < tiles; t += pairs) {
       const Tile c = tile_at(t, mt, p.n_tiles, p.splits, kblocks);
-      const int b = tc & 1;
-      const bool got = wait(&accfull[b], (tc >> 1) & 1);
-      if (!got && lane == 0) fail(p, kErrTimeout);
-      ptx::tc_fence_after();
-      const uint32_t tbase = tmem + (static_cast<uint32_t>(q * 32) << 16) + b * kTile + h * kHalf;
+      const int steps = kProds * (c.kb1 - c.kb0);
       const int row0 = c.m * kTile + static_cast<int>(rank) * kHalf + q * 32;   // this warp's first row
       const int row = row0 + lane;
-      const int col0 = c.n * kTile + h * kHalf;                                 // and column of the tile grid
+      const int col0 = c.n * kTile + h * kCols;   // and column, within the piece
 
-      if (EPI == STATS) {
-        const int label = row < n_live ? __ldcg(p.labels + row) : -1;
-        float m = -INFINITY, s = 0.0f;
-#pragma unroll 1
-        for (int cc = 0; cc < kHalf; cc += 32) {
-          float v[32];
-          ptx::tmem_ld32(tbase + cc, v);
-          const int c0 = col0 + cc;
-          if (c0 + 32 > p.V) {
+      // the sum of the chunks (every warp walks all of them even after a failed wait, whose
+      // successors then return at once, so that the barriers below are reached by all)
+      // (bf16 results of one chunk are read out 16 columns at a time further down instead)
+      constexpr bool kStream = (EPI == DH || EPI == DW) && PLANES == 1;
+      float v[kCols];
+      int i = 0;
+      do {
+        const int b = ch & 1;
+        const bool got = wait(&accfull[b], (ch >> 1) & 1);
+        if (!got && lane == 0) fail(p, kErrTimeout);
+        ptx::tc_fence_after();
+        if (kStream) break;
+        const uint32_t tbase = tmem + (static_cast<uint32_t>(q * 32) << 16) + b * kTile + h * kCols;
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (c0 + j >= p.V) v[j] = -INFINITY;
-          }
-          if (label >= c0 && label < c0 + 32) {
+        for (int cc = 0; cc < kCols; cc += 8) {
+          float x[8];
+          ptx::tmem_ld8(tbase + cc, x);
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (label == c0 + j) p.target[row] = v[j];
-          }
-          float mm = m;
-#pragma unroll
-          for (int j = 0; j < 32; ++j) mm = fmaxf(mm, v[j]);
-          const float r = mm == -INFINITY ? 0.0f : mm;   // nothing but -inf so far: sums stay 0
-          s *= ex2((m - r) * kLog2e);
-#pragma unroll
-          for (int j = 0; j < 32; ++j) s += ex2((v[j] - r) * kLog2e);
-          m = mm;
+          for (int j = 0; j < 8; ++j) v[cc + j] = i == 0 ? x[j] : v[cc + j] + x[j];
         }
-        if (row < n_live) p.parts[static_cast<int64_t>(2 * c.n + h) * p.n_pad + row] = make_float2(m, s);
-      } else if (EPI == GRAD) {
+        release();
+        i = steps - i > kChunk ? i + kChunk : steps;
+      } while (i < steps);
+
+      if (EPI == STATS || EPI == EXP || EPI == GRAD) {
         const bool live = row < n_live;
         const int label = live ? __ldcg(p.labels + row) - p.v0 : -1;
-        const float w = live ? __ldcg(p.weights + row) : 0.0f;
-        const float lse = live ? __ldcg(p.lse + row) : 0.0f;
-#pragma unroll 1
-        for (int cc = 0; cc < kHalf; cc += 64) {
-          float v[64];
-          ptx::tmem_ld64(tbase + cc, v);
-          const int c0 = col0 + cc;
+        const int left = p.V - p.v0 - col0;   // columns of this warp that exist
+        float2 part = make_float2(0.0f, 0.0f);
+        if (EPI == STATS) {
+          if (left < kCols) {
 #pragma unroll
-          for (int j = 0; j < 64; ++j) v[j] = w * ex2((v[j] - lse) * kLog2e);
-          if (label >= c0 && label < c0 + 64) {
-#pragma unroll
-            for (int j = 0; j < 64; ++j)
-              if (label == c0 + j) v[j] -= w;
+            for (int j = 0; j < kCols; ++j)
+              if (j >= left) v[j] = -INFINITY;
           }
-          if (!live || p.v0 + c0 + 64 > p.V) {   // rows and columns that only fill up the tile
+          if (label >= col0 && label < col0 + kCols) {
 #pragma unroll
-            for (int j = 0; j < 64; ++j)
-              if (!live || p.v0 + c0 + j >= p.V) v[j] = 0.0f;
+            for (int j = 0; j < kCols; ++j)
+              if (label == col0 + j) p.target[row] = v[j];
+          }
+          float m = v[0];
+#pragma unroll
+          for (int j = 1; j < kCols; ++j) m = fmaxf(m, v[j]);
+          const float r = m == -INFINITY ? 0.0f : m;   // nothing but -inf: the sum stays 0
+          float s = 0.0f;
+#pragma unroll
+          for (int j = 0; j < kCols; ++j) s += ex2((v[j] - r) * kLog2e);
+          part = make_float2(m, s);
+        } else {
+          const float w = EPI == GRAD && live ? __ldcg(p.weights + row) : 1.0f;
+          const float r = live ? __ldcg((EPI == GRAD ? p.lse : p.ref) + row) : 0.0f;
+          if (EPI == EXP && label >= col0 && label < col0 + kCols) {
+#pragma unroll
+            for (int j = 0; j < kCols; ++j)
+              if (label == col0 + j) {
+                p.target[row] = v[j] - r;
+                v[j] = -INFINITY;   // left out of the sums
+              }
+          }
+#pragma unroll
+          for (int j = 0; j < kCols; ++j) v[j] = w * ex2((v[j] - r) * kLog2e);
+          if (EPI == GRAD && label >= col0 && label < col0 + kCols) {
+#pragma unroll
+            for (int j = 0; j < kCols; ++j)
+              if (label == col0 + j) v[j] -= w;
+          }
+          if (!live || left < kCols) {   // rows and columns that only fill up the tile
+#pragma unroll
+            for (int j = 0; j < kCols; ++j)
+              if (!live || j >= left) v[j] = 0.0f;
+          }
+          if (EPI == EXP) {
+            float s = 0.0f;
+#pragma unroll
+            for (int j = 0; j < kCols; ++j) s += v[j];
+            if (s > kExpLimit) atomicOr(&p.state->retry, 1);
+            part = make_float2(s, 0.0f);
           }
 #pragma unroll
           for (int pl = 0; pl < PLANES; ++pl) {
-            // the warp's 32 rows x 64 columns through its box, so that whole 128-byte lines are
-            // written: unit u of row r sits at u ^ (r & 7)
-            __syncwarp();
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-              uint4 x;
-              x.x = pack2(v[8 * u + 0], v[8 * u + 1]);
-              x.y = pack2(v[8 * u + 2], v[8 * u + 3]);
-              x.z = pack2(v[8 * u + 4], v[8 * u + 5]);
-              x.w = pack2(v[8 * u + 6], v[8 * u + 7]);
-              box4[lane * 8 + (u ^ (lane & 7))] = x;
+            for (int half = 0; half < kCols; half += 32) {
+              // the warp's 32 rows x 32 columns through its box, so that pieces of 64 bytes are
+              // written: unit u of row r sits at u ^ (r / 2 % 4)
+              uint4* box4 = reinterpret_cast<uint4*>(box);
+              __syncwarp();
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                const int j = half + 8 * u;
+                box4[lane * 4 + (u ^ ((lane >> 1) & 3))] =
+                    make_uint4(pack2(v[j], v[j + 1]), pack2(v[j + 2], v[j + 3]), pack2(v[j + 4], v[j + 5]),
+                               pack2(v[j + 6], v[j + 7]));
+              }
+              __syncwarp();
+              const int u = lane & 3;
+              __nv_bfloat16* dst = p.g + static_cast<int64_t>(row0) * p.ldg + static_cast<int64_t>(pl) * p.planeG + col0 +
+                                   half + 8 * u;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int rr = 8 * k + (lane >> 2);
+                *reinterpret_cast<uint4*>(dst + rr * p.ldg) = box4[rr * 4 + (u ^ ((rr >> 1) & 3))];
+              }
             }
             if (pl + 1 < PLANES) {
 #pragma unroll
-              for (int j = 0; j < 64; ++j) v[j] -= __bfloat162float(__float2bfloat16_rn(v[j]));
-            }
-            __syncwarp();
-            const int u = lane & 7;
-            __nv_bfloat16* dst = p.g + static_cast<int64_t>(row0) * p.ldg +
-                                 static_cast<int64_t>(pl) * p.planeG + c0 + 8 * u;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int rr = 4 * i + (lane >> 3);
-              *reinterpret_cast<uint4*>(dst + rr * p.ldg) = box4[rr * 8 + (u ^ (rr & 7))];
+              for (int j = 0; j < kCols; ++j) v[j] -= __bfloat162float(__float2bfloat16_rn(v[j]));
             }
           }
         }
-      } else {   // DH, DW: 32 columns at a time through the box
-        const bool have = c.kb1 > c.kb0;
+        if (EPI != GRAD) {
+          // the row's four parts, one per warp of its lane quarter, joined in order
+          __syncwarp();   // the box has been read out
+          *part_of(h) = part;
+          epi_bar();
+          if (h == 0 && live) {
+            float2 x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[k] = *part_of(k);
+            float2 y;
+            if (EPI == EXP) {
+              y = make_float2(((x[0].x + x[1].x) + x[2].x) + x[3].x, 0.0f);
+            } else {
+              const float m = fmaxf(fmaxf(x[0].x, x[1].x), fmaxf(x[2].x, x[3].x));
+              const float r = m == -INFINITY ? 0.0f : m;
+              float s = 0.0f;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) s += x[k].y * ex2((x[k].x - r) * kLog2e);
+              y = make_float2(m, s);
+            }
+            p.parts[static_cast<int64_t>(p.v0 / kTile + c.n) * p.n_pad + row] = y;
+          }
+          epi_bar();   // the boxes may be written again
+        }
+      } else {   // DH, DW: 16 columns at a time through the box
+        using T = typename HeadType<PLANES>::T;
+        const bool have = steps > 0;
         const int M = EPI == DH ? n_live : p.V - p.v0;   // rows that exist
         float* acc = EPI == DH && p.acc ? p.acc + static_cast<int64_t>(c.s) * p.n_pad * p.ldacc : nullptr;
-#pragma unroll 1
-        for (int cc = 0; cc < kHalf; cc += 32) {
-          float v[32];
-          ptx::tmem_ld32(tbase + cc, v);
-          const int c0 = col0 + cc;
-          if (c0 >= p.d) continue;
+        float4* f4 = reinterpret_cast<float4*>(box);
+        auto put16 = [&](int cc, const float* x16) {
           __syncwarp();
-          float4* f4 = reinterpret_cast<float4*>(box);
 #pragma unroll
-          for (int u = 0; u < 8; ++u)
-            f4[lane * 8 + (u ^ (lane & 7))] = have ? make_float4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3])
-                                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int u = 0; u < 4; ++u)
+            f4[lane * 4 + (u ^ ((lane >> 1) & 3))] =
+                have ? make_float4(x16[4 * u], x16[4 * u + 1], x16[4 * u + 2], x16[4 * u + 3])
+                     : make_float4(0.f, 0.f, 0.f, 0.f);
           __syncwarp();
-          const int u = lane & 7, col = c0 + 4 * u;
+          const int u = lane & 3, col = col0 + cc + 4 * u;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int rr = 4 * i + (lane >> 3), r = row0 + rr;
+          for (int k = 0; k < 4; ++k) {
+            const int rr = 8 * k + (lane >> 2), r = row0 + rr;
             if (r >= M || col >= p.d) continue;
-            float4 x = f4[rr * 8 + (u ^ (rr & 7))];
+            const float4 x4 = f4[rr * 4 + (u ^ ((rr >> 1) & 3))];
+            float x[4] = {x4.x, x4.y, x4.z, x4.w};
             if (EPI == DH && acc) {
               float4* a = reinterpret_cast<float4*>(acc + r * p.ldacc + col);
               if (p.add) {
                 const float4 y = *a;
-                x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+                x[0] += y.x, x[1] += y.y, x[2] += y.z, x[3] += y.w;
               }
               if (!p.last) {
-                *a = x;
+                *a = make_float4(x[0], x[1], x[2], x[3]);
                 continue;
               }
             }
-            const int64_t orow = EPI == DH ? __ldcg(p.rows + r) : p.v0 + r;
-            if (PLANES == 3) {
-              float* o = static_cast<float*>(p.out) + orow * p.d + col;
-              if (p.d % 4 == 0) {
-                *reinterpret_cast<float4*>(o) = x;
-              } else {
-                const float e[4] = {x.x, x.y, x.z, x.w};
+            if (EPI == DH && p.coef) {
+              const float2 co = __ldcg(p.coef + r);
+              const T* wl = static_cast<const T*>(p.W) + static_cast<int64_t>(__ldcg(p.labels + r)) * p.d + col;
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  if (col + k < p.d) o[k] = e[k];
-              }
-            } else {
-              __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + orow * p.d + col;
-              if (p.d % 4 == 0) {
-                *reinterpret_cast<uint2*>(o) = make_uint2(pack2(x.x, x.y), pack2(x.z, x.w));
-              } else {
-                const float e[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  if (col + k < p.d) o[k] = __float2bfloat16_rn(e[k]);
-              }
+              for (int e = 0; e < 4; ++e)
+                if (col + e < p.d) x[e] = co.x * x[e] - co.y * static_cast<float>(wl[e]);
             }
+            const int64_t orow = EPI == DH ? __ldcg(p.rows + r) : p.v0 + r;
+            store4(static_cast<T*>(p.out) + orow * p.d + col, x, col, p.d);
           }
+        };
+        if (kStream) {
+          const uint32_t tbase = tmem + (static_cast<uint32_t>(q * 32) << 16) + (ch & 1) * kTile + h * kCols;
+#pragma unroll 1
+          for (int cc = 0; cc < kCols; cc += 16) {
+            float x[16];
+            ptx::tmem_ld16(tbase + cc, x);
+            if (col0 + cc < p.d) put16(cc, x);
+          }
+          release();
+        } else {
+#pragma unroll
+          for (int cc = 0; cc < kCols; cc += 16)
+            if (col0 + cc < p.d) put16(cc, v + cc);
         }
       }
-      // this accumulator may be overwritten by the tile after next
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive_cluster(ptx::cluster_addr(&accempty[b], 0));
     }
   }
 
@@ -481,7 +620,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   ptx::tc_fence_before();
   __syncthreads();
   ptx::cluster_sync();   // the peer's arrivals on this CTA's barriers are in
-  if (warp == 1) {
+  if (warp == kMmaWarp) {
     __syncwarp();
     ptx::tc_fence_after();
     ptx::tmem_dealloc_pair(tmem, 512);
@@ -497,40 +636,58 @@ __device__ __forceinline__ int label_at(const void* labels, int id_bytes, int64_
 }
 
 // The live rows in order, then the dropped ones from the end backwards: rows[0 .. n_live) and
-// rows[N-1], rows[N-2], ...  One CTA; dropped rows' losses are zeroed here.
+// rows[N-1], rows[N-2], ...  One CTA, 8192 rows at a time with all their loads in flight; dropped
+// rows' losses are zeroed here.
+constexpr int kRowsPer = 8;
 __global__ void __launch_bounds__(1024) head_rows_kernel(const void* labels, int id_bytes, const float* weights,
                                                          int N, int V, HeadState* state, int* rows, int* lab, float* wgt,
                                                          float* loss) {
   ptx::griddep_launch_dependents();
-  __shared__ int wtot[32];
+  __shared__ int tot[kRowsPer * 32], scan[kRowsPer * 32 + 1], wsum[kRowsPer];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int done = 0;   // live rows so far
-  for (int n0 = 0; n0 < N; n0 += 1024) {
-    const int n = n0 + tid;
-    int label = -1;
-    float w = 0.0f;
-    if (n < N) {
-      label = label_at(labels, id_bytes, n, V);
-      w = weights ? weights[n] : 1.0f;
-    }
-    const bool live = label >= 0 && w != 0.0f;
-    const uint32_t m = __ballot_sync(0xffffffffu, live);
-    if (lane == 0) wtot[warp] = __popc(m);
-    __syncthreads();
-    int before = 0, all = 0;
+  for (int n0 = 0; n0 < N; n0 += 1024 * kRowsPer) {
+    int label[kRowsPer];
+    float w[kRowsPer];
 #pragma unroll
-    for (int k = 0; k < 32; ++k) {
-      before += k < warp ? wtot[k] : 0;
-      all += wtot[k];
+    for (int k = 0; k < kRowsPer; ++k) {
+      const int n = n0 + k * 1024 + tid;
+      label[k] = n < N ? label_at(labels, id_bytes, n, V) : -1;
+      w[k] = n < N && weights ? weights[n] : 1.0f;
     }
-    const int at = done + before + __popc(m & ((1u << lane) - 1));
-    if (live) {
-      rows[at] = n;
-      lab[at] = label;
-      wgt[at] = w;
-    } else if (n < N) {
-      rows[N - 1 - (n - at)] = n;   // n - at dropped rows come before this one
-      loss[n] = 0.0f;
+    uint32_t m[kRowsPer];
+#pragma unroll
+    for (int k = 0; k < kRowsPer; ++k) {
+      m[k] = __ballot_sync(0xffffffffu, label[k] >= 0 && w[k] != 0.0f);
+      if (lane == 0) tot[k * 32 + warp] = __popc(m[k]);
+    }
+    __syncthreads();
+    if (tid < kRowsPer * 32) {   // exclusive scan of the 256 counts
+      const int x = tot[tid];
+      int incl = x;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      scan[tid] = incl - x;
+      if (lane == 31) wsum[warp] = incl;
+    }
+    __syncthreads();
+    int all = 0;
+#pragma unroll
+    for (int k = 0; k < kRowsPer; ++k) {
+      const int n = n0 + k * 1024 + tid;
+      const int at = done + all + scan[k * 32 + warp] + __popc(m[k] & ((1u << lane) - 1));
+      if (label[k] >= 0 && w[k] != 0.0f) {
+        rows[at] = n;
+        lab[at] = label[k];
+        wgt[at] = w[k];
+      } else if (n < N) {
+        rows[N - 1 - (n - at)] = n;   // n - at dropped rows come before this one
+        loss[n] = 0.0f;
+      }
+      all += wsum[k];
     }
     done += all;
     __syncthreads();
@@ -538,28 +695,47 @@ __global__ void __launch_bounds__(1024) head_rows_kernel(const void* labels, int
   if (tid == 0) {
     state->err = 0;
     state->n_live = done;
+    state->retry = 0;
   }
 }
 
 // Row r of the compact H (bf16, or three planes of fp32), a CTA per row: the live rows, then zero
-// rows up to a whole tile.  Dropped rows of dH are zeroed.
+// rows up to a whole tile; nothing where the products can read H itself (`direct` and every row
+// live).  Dropped rows of dH are zeroed.  ref (not null): the label's logit of each live row.
 template <class T, int PLANES>
 __global__ void __launch_bounds__(128) head_gather_kernel(const T* H, int d, int64_t N, const HeadState* state,
-                                                          const int* rows, __nv_bfloat16* Hc, int plane, T* dH) {
+                                                          const int* rows, __nv_bfloat16* Hc, int plane, T* dH,
+                                                          int direct, const T* W, const int* labels, float* ref) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
+  __shared__ float red[4];
   const int64_t r = blockIdx.x;
   const int n_live = __ldcg(&state->n_live);
   const int64_t fill = (static_cast<int64_t>(n_live) + kTile - 1) / kTile * kTile;
+  const bool copy = !(direct && n_live == N);
   __nv_bfloat16* dst = Hc + r * plane * PLANES;
   if (r < n_live) {
     const T* src = H + static_cast<int64_t>(__ldcg(rows + r)) * d;
+    const T* wl = ref ? W + static_cast<int64_t>(__ldcg(labels + r)) * d : nullptr;
+    float dot = 0.0f;
     if (PLANES == 1 && d % 8 == 0) {
-      for (int c = threadIdx.x; c < d / 8; c += 128)
-        reinterpret_cast<uint4*>(dst)[c] = reinterpret_cast<const uint4*>(src)[c];
+      for (int c = threadIdx.x; c < d / 8; c += 128) {
+        const uint4 x = reinterpret_cast<const uint4*>(src)[c];
+        if (copy) reinterpret_cast<uint4*>(dst)[c] = x;
+        if (ref) {
+          const uint4 y = reinterpret_cast<const uint4*>(wl)[c];
+          const uint32_t a[4] = {x.x, x.y, x.z, x.w}, b[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            dot = fmaf(__uint_as_float(a[k] << 16), __uint_as_float(b[k] << 16), dot);
+            dot = fmaf(__uint_as_float(a[k] & 0xffff0000u), __uint_as_float(b[k] & 0xffff0000u), dot);
+          }
+        }
+      }
     } else {
       for (int c = threadIdx.x; c < plane; c += 128) {
         float x = c < d ? static_cast<float>(src[c]) : 0.0f;
+        if (ref && c < d) dot = fmaf(x, static_cast<float>(wl[c]), dot);
 #pragma unroll
         for (int k = 0; k < PLANES; ++k) {
           const __nv_bfloat16 b = __float2bfloat16_rn(x);
@@ -568,9 +744,16 @@ __global__ void __launch_bounds__(128) head_gather_kernel(const T* H, int d, int
         }
       }
     }
+    if (ref) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+      if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = dot;
+      __syncthreads();
+      if (threadIdx.x == 0) ref[r] = (red[0] + red[1]) + (red[2] + red[3]);
+    }
     return;
   }
-  if (r < fill)
+  if (copy && r < fill)
     for (int c = threadIdx.x; c < plane * PLANES / 8; c += 128) reinterpret_cast<uint4*>(dst)[c] = make_uint4(0, 0, 0, 0);
   if (r < N && dH) {
     T* o = dH + static_cast<int64_t>(__ldcg(rows + r)) * d;
@@ -596,12 +779,17 @@ __global__ void __launch_bounds__(128) head_weights_kernel(const T* W, int d, __
   }
 }
 
-// lse and loss of 32 rows per CTA: eight threads share a row's partial sums, joined in order.
-__global__ void __launch_bounds__(256) head_loss_kernel(const HeadState* state, const float2* parts, int slots,
-                                                        int64_t n_pad, const float* target, const float* weights,
-                                                        const int* rows, float* lse, float* loss) {
+// The losses, from the rows' partial sums, 32 rows per CTA: eight threads share a row's parts, eight
+// loads of each in flight, joined in a fixed order.  After STATS (EXPS false): lse and loss.  After
+// EXP: loss, and the coefficients of dH.
+template <bool EXPS>
+__global__ void __launch_bounds__(256) head_loss_kernel(const HeadState* state, int only_retry, const float2* parts,
+                                                        int slots, int64_t n_pad, const float* target,
+                                                        const float* weights, const int* rows, float* lse,
+                                                        float2* coef, float* loss) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
+  if (only_retry && __ldcg(&state->retry) == 0) return;
   __shared__ float2 red[8][32];
   const int lane = threadIdx.x & 31, part = threadIdx.x >> 5;
   const int n_live = __ldcg(&state->n_live);
@@ -614,54 +802,92 @@ __global__ void __launch_bounds__(256) head_loss_kernel(const HeadState* state, 
     m = mm;
   };
   if (row < n_live)
-    for (int k = part; k < slots; k += 8) {
-      const float2 x = __ldcg(parts + k * n_pad + row);
-      join(x.x, x.y);
+    for (int k0 = part; k0 < slots; k0 += 64) {
+      float2 x[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        x[u] = k0 + 8 * u < slots ? __ldcg(parts + (k0 + 8 * u) * n_pad + row)
+                                  : make_float2(EXPS ? 0.0f : -INFINITY, 0.0f);
+      if (EXPS) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) s += x[u].x;
+      } else {
+        float mm = m;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) mm = fmaxf(mm, x[u].x);
+        const float r = mm == -INFINITY ? 0.0f : mm;
+        s *= ex2((m - r) * kLog2e);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) s += x[u].y * ex2((x[u].x - r) * kLog2e);
+        m = mm;
+      }
     }
   red[part][lane] = make_float2(m, s);
   __syncthreads();
   if (part == 0 && row < n_live) {
-    m = -INFINITY;
-    s = 0.0f;
+    const float w = __ldcg(weights + row), t = __ldcg(target + row);
+    float x;
+    if (EXPS) {
+      s = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) join(red[k][lane].x, red[k][lane].y);
-    const float l = m + logf(s);
-    lse[row] = l;
-    // log(s) - (target - m) rather than lse - target: the difference of the two large ones is exact
-    float x = __ldcg(weights + row) * (logf(s) - (__ldcg(target + row) - m));
+      for (int k = 0; k < 8; ++k) s += red[k][lane].y;
+      const float el = ex2(t * kLog2e), inv = 1.0f / (s + el);
+      coef[row] = make_float2(w * inv, w * (s * inv));
+      x = w * log1pf(s / el);
+    } else {
+      m = -INFINITY;
+      s = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) join(red[k][lane].x, red[k][lane].y);
+      lse[row] = m + logf(s);
+      // log(s) - (target - m) rather than lse - target: the difference of the two large ones is exact
+      x = w * (logf(s) - (t - m));
+    }
     if (__ldcg(&state->err)) x = __int_as_float(0x7fc00000);
     loss[__ldcg(rows + row)] = x;
   }
 }
 
-// dH from the splits of the vocabulary, added in order.
+// dH from the splits of the vocabulary, added in order (and, after EXP, the coefficients applied).
 template <class T>
-__global__ void __launch_bounds__(256) head_join_kernel(const HeadState* state, const float* acc, int splits,
-                                                        int64_t n_pad, int64_t ldacc, int d, const int* rows, T* dH) {
+__global__ void __launch_bounds__(256) head_join_kernel(const HeadState* state, int only_retry, const float* acc,
+                                                        int splits, int64_t n_pad, int64_t ldacc, int d,
+                                                        const int* rows, const float2* coef, const int* labels,
+                                                        const T* W, T* dH) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
+  if (only_retry && __ldcg(&state->retry) == 0) return;
   const int n_live = __ldcg(&state->n_live);
   for (int64_t r = blockIdx.y; r < n_live; r += gridDim.y) {
     const int c = blockIdx.x * 256 + threadIdx.x;
     if (c >= d) continue;
     float x = 0.0f;
     for (int s = 0; s < splits; ++s) x += __ldcg(acc + (s * n_pad + r) * ldacc + c);
+    if (coef) {
+      const float2 co = __ldcg(coef + r);
+      x = co.x * x - co.y * static_cast<float>(W[static_cast<int64_t>(__ldcg(labels + r)) * d + c]);
+    }
     dH[static_cast<int64_t>(__ldcg(rows + r)) * d + c] = static_cast<T>(x);
   }
 }
 
 // ---- host ---------------------------------------------------------------------------------------
 
+// From this many multiplications N d V on, dH alone takes one pass: the product it saves is worth more
+// than the launches behind it that leave at once.
+constexpr double kOnePassWork = 1.0e10;
+
 struct HeadPlan {
   int planes, plane;       // bf16 planes of an operand; elements of a plane's row
   bool copy_W;
   int64_t n_pad;
-  int slots;               // 128-column slots of the vocabulary
+  int slots;               // tiles of the vocabulary: one partial sum per row each
   int piece, pieces;       // columns of a piece (a multiple of 256), pieces
   int splits;              // of DH
   bool acc;                // DH goes through fp32 memory
   int64_t ldacc;
-  size_t o_rows, o_labels, o_weights, o_lse, o_target, o_parts, o_H, o_W, o_g, o_acc, bytes;
+  bool one_pass;           // EXP
+  size_t o_rows, o_labels, o_weights, o_lse, o_coef, o_target, o_parts, o_H, o_W, o_g, o_acc, bytes;
 
   explicit HeadPlan(const HeadShape& s) {
     planes = s.dtype == GRAPE_F32 ? 3 : 1;
@@ -669,7 +895,8 @@ struct HeadPlan {
     plane = planes == 3 ? (s.d + 63) / 64 * 64 : (s.d + 7) / 8 * 8;
     copy_W = planes == 3 || plane != s.d;
     n_pad = (s.N + kTile - 1) / kTile * kTile;
-    slots = (s.V + kTile - 1) / kTile * 2;
+    slots = (s.V + kTile - 1) / kTile;
+    one_pass = s.dH && !s.dW && static_cast<double>(s.N) * s.d * s.V >= kOnePassWork;
     const int64_t vmax = (static_cast<int64_t>(s.V) + kTile - 1) / kTile * kTile;
     int64_t cols = static_cast<int64_t>(kPieceBytes / (std::max<int64_t>(n_pad, 1) * 2 * planes)) / kTile * kTile;
     cols = std::min(std::max<int64_t>(cols, 4096), vmax);
@@ -697,6 +924,7 @@ struct HeadPlan {
     o_weights = take(np * 4);
     o_lse = take(np * 4);
     o_target = take(np * 4);
+    o_coef = take(one_pass ? np * 8 : 0);
     o_parts = take(np * slots * 8);
     o_H = take(np * plane * planes * 2);
     o_W = take(copy_W ? static_cast<size_t>(s.V) * plane * planes * 2 : 0);
@@ -748,96 +976,140 @@ cudaError_t run_head(const HeadShape& s, const T* H, const T* W, const void* lab
   const int wide = pl.plane * PLANES;
   const int64_t gw = static_cast<int64_t>(pl.piece) * PLANES;
 
+  float2* coef = pl.one_pass ? reinterpret_cast<float2*>(ws + pl.o_coef) : nullptr;
+  const int direct = PLANES == 1 && !pl.copy_W;   // H itself can be an operand when every row is live
+
   cudaError_t e = launch(false, head_rows_kernel, dim3(1), 1024, 0, st, labels, id_bytes, weights,
                          static_cast<int>(s.N), s.V, state, rows, lab, wgt, loss);
   if (e == cudaSuccess && s.N > 0)
     e = launch(true, head_gather_kernel<T, PLANES>, dim3(static_cast<unsigned>(pl.n_pad)), 128, 0, st, H, s.d, s.N,
-               static_cast<const HeadState*>(state), static_cast<const int*>(rows), Hc, pl.plane, dH);
+               static_cast<const HeadState*>(state), static_cast<const int*>(rows), Hc, pl.plane, dH, direct, W,
+               static_cast<const int*>(lab), pl.one_pass ? lse : nullptr);
   if (e == cudaSuccess && pl.copy_W)
     e = launch(true, head_weights_kernel<T, PLANES>, dim3(s.V), 128, 0, st, W, s.d, Wc, pl.plane);
   if (e != cudaSuccess) return e;
   if (s.N == 0) return dW ? cudaMemsetAsync(dW, 0, static_cast<size_t>(s.V) * s.d * sizeof(T), st) : cudaSuccess;
 
   // operand views: K-major boxes of 64 x 128 rows, M/N-major boxes of 64 x 64
-  CUtensorMap H_k, H_mn, W_k, W_mn, g_k, g_mn;
-  if (!tc_map_2d(&H_k, Hc, pl.n_pad, wide, wide, kBK, kHalf) || !tc_map_2d(&W_k, Wc, s.V, wide, wide, kBK, kHalf))
-    return cudaErrorInvalidValue;
-  HeadGemm p;
-  std::memset(&p, 0, sizeof(p));
-  p.state = state;
-  p.V = s.V;
-  p.d = s.d;
-  p.n_pad = pl.n_pad;
-  p.labels = lab;
-  p.weights = wgt;
-  p.lse = lse;
-  p.parts = parts;
-  p.target = target;
-  p.g = g;
-  p.ldg = gw;
-  p.planeG = pl.piece;
-  p.rows = rows;
-  p.poison = loss;
-  p.n_rows = s.N;
-  p.splits = 1;
+  const bool grads = s.dH || s.dW;
+  CUtensorMap H_k, H_mn, W_k, W_mn, g_k, g_mn, X_k, X_mn;
+  std::memset(&X_k, 0, sizeof(X_k));
+  std::memset(&X_mn, 0, sizeof(X_mn));
+  bool ok = tc_map_2d(&H_k, Hc, pl.n_pad, wide, wide, kBK, kHalf) && tc_map_2d(&W_k, Wc, s.V, wide, wide, kBK, kHalf);
+  if (ok && direct) ok = tc_map_2d(&X_k, H, s.N, wide, wide, kBK, kHalf) && tc_map_2d(&X_mn, H, s.N, wide, wide, 64, kBK);
+  if (ok && grads)
+    ok = tc_map_2d(&H_mn, Hc, pl.n_pad, wide, wide, 64, kBK) && tc_map_2d(&W_mn, Wc, s.V, wide, wide, 64, kBK) &&
+         tc_map_2d(&g_k, g, pl.n_pad, gw, gw, kBK, kHalf) && tc_map_2d(&g_mn, g, pl.n_pad, gw, gw, 64, kBK);
+  if (!ok) return cudaErrorInvalidValue;
 
+  HeadGemm base;
+  std::memset(&base, 0, sizeof(base));
+  base.state = state;
+  base.V = s.V;
+  base.d = s.d;
+  base.n_pad = pl.n_pad;
+  base.labels = lab;
+  base.weights = wgt;
+  base.lse = base.ref = lse;
+  base.parts = parts;
+  base.target = target;
+  base.g = g;
+  base.ldg = gw;
+  base.planeG = pl.piece;
+  base.rows = rows;
+  base.poison = loss;
+  base.n_rows = s.N;
+  base.splits = 1;
   const int64_t mt = pl.n_pad / kTile;
-  p.mapA = H_k;
-  p.mapB = W_k;
-  p.planeA = p.planeB = pl.plane;
-  p.kblocks = (pl.plane + kBK - 1) / kBK;
-  p.n_tiles = pl.slots / 2;
-  e = run_gemm<STATS, PLANES>(p, mt * p.n_tiles, st);
-  if (e == cudaSuccess)
-    e = launch(true, head_loss_kernel, dim3(static_cast<unsigned>((s.N + 31) / 32)), 256, 0, st,
-               static_cast<const HeadState*>(state), static_cast<const float2*>(parts), pl.slots, pl.n_pad,
-               static_cast<const float*>(target), static_cast<const float*>(wgt), static_cast<const int*>(rows), lse,
-               loss);
-  if (e != cudaSuccess || (!s.dH && !s.dW)) return e;
-
-  if (!tc_map_2d(&H_mn, Hc, pl.n_pad, wide, wide, 64, kBK) || !tc_map_2d(&W_mn, Wc, s.V, wide, wide, 64, kBK) ||
-      !tc_map_2d(&g_k, g, pl.n_pad, gw, gw, kBK, kHalf) || !tc_map_2d(&g_mn, g, pl.n_pad, gw, gw, 64, kBK))
-    return cudaErrorInvalidValue;
   const int dt = (s.d + kTile - 1) / kTile;
-  for (int i = 0; i < pl.pieces; ++i) {
-    const int v0 = i * pl.piece, cols = std::min(pl.piece, s.V - v0), vt = (cols + kTile - 1) / kTile;
-    HeadGemm q = p;
-    q.v0 = v0;
-    q.n_tiles = vt;
-    e = run_gemm<GRAD, PLANES>(q, mt * vt, st);
-    if (e != cudaSuccess) return e;
-    if (s.dH) {
-      HeadGemm y = q;
-      y.mapA = g_k;
-      y.mapB = W_mn;
-      y.planeA = pl.piece;
-      y.kblocks = (cols + kBK - 1) / kBK;
-      y.n_tiles = dt;
-      y.splits = pl.splits;
-      y.acc = pl.acc ? reinterpret_cast<float*>(ws + pl.o_acc) : nullptr;
-      y.ldacc = pl.ldacc;
-      y.add = i > 0;
-      y.last = i + 1 == pl.pieces && pl.splits == 1;
-      y.out = dH;
-      e = run_gemm<DH, PLANES>(y, mt * dt * pl.splits, st);
-      if (e != cudaSuccess) return e;
-    }
-    if (s.dW) {
-      HeadGemm x = q;
-      x.mapA = g_mn;
-      x.mapB = H_mn;
-      x.planeA = pl.piece;
-      x.m_tiles = vt;
-      x.n_tiles = dt;
-      x.out = dW;
-      e = run_gemm<DW, PLANES>(x, static_cast<int64_t>(vt) * dt, st);
+
+  // z of the vocabulary rows from v0 on (`cols` of them)
+  auto logits = [&](int v0, int cols) {
+    HeadGemm p = base;
+    p.mapA = H_k;
+    p.mapB = W_k;
+    p.mapH = X_k;
+    p.direct = direct;
+    p.planeA = p.planeB = pl.plane;
+    p.kblocks = (pl.plane + kBK - 1) / kBK;
+    p.v0 = v0;
+    p.n_tiles = (cols + kTile - 1) / kTile;
+    return p;
+  };
+  auto losses = [&](bool exps, int only_retry) {
+    const dim3 grid(static_cast<unsigned>((s.N + 31) / 32));
+    auto go = [&](auto kernel) {
+      return launch(true, kernel, grid, 256, 0, st, static_cast<const HeadState*>(state), only_retry,
+                    static_cast<const float2*>(parts), pl.slots, pl.n_pad, static_cast<const float*>(target),
+                    static_cast<const float*>(wgt), static_cast<const int*>(rows), lse, coef, loss);
+    };
+    return exps ? go(head_loss_kernel<true>) : go(head_loss_kernel<false>);
+  };
+  auto input_grad = [&](int i, int v0, int cols, bool exps, int only_retry) {
+    HeadGemm p = base;
+    p.only_retry = only_retry;
+    p.mapA = g_k;
+    p.mapB = W_mn;
+    p.planeA = pl.piece;
+    p.planeB = pl.plane;
+    p.kblocks = (cols + kBK - 1) / kBK;
+    p.v0 = v0;
+    p.n_tiles = dt;
+    p.splits = pl.splits;
+    p.acc = pl.acc ? reinterpret_cast<float*>(ws + pl.o_acc) : nullptr;
+    p.ldacc = pl.ldacc;
+    p.add = i > 0;
+    p.last = i + 1 == pl.pieces && pl.splits == 1;
+    p.coef = exps ? coef : nullptr;
+    p.W = W;
+    p.out = dH;
+    cudaError_t e2 = run_gemm<DH, PLANES>(p, mt * dt * pl.splits, st);
+    if (e2 == cudaSuccess && i + 1 == pl.pieces && pl.splits > 1)
+      e2 = launch(true, head_join_kernel<T>,
+                  dim3((s.d + 255) / 256, static_cast<unsigned>(std::min<int64_t>(s.N, 4096))), 256, 0, st,
+                  static_cast<const HeadState*>(state), only_retry, reinterpret_cast<const float*>(ws + pl.o_acc),
+                  pl.splits, pl.n_pad, pl.ldacc, s.d, static_cast<const int*>(rows), p.coef,
+                  static_cast<const int*>(lab), W, dH);
+    return e2;
+  };
+
+  if (pl.one_pass) {
+    for (int i = 0; i < pl.pieces; ++i) {
+      const int v0 = i * pl.piece, cols = std::min(pl.piece, s.V - v0);
+      HeadGemm p = logits(v0, cols);
+      e = run_gemm<EXP, PLANES>(p, mt * p.n_tiles, st);
+      if (e == cudaSuccess && i + 1 == pl.pieces) e = losses(true, 0);
+      if (e == cudaSuccess) e = input_grad(i, v0, cols, true, 0);
       if (e != cudaSuccess) return e;
     }
   }
-  if (s.dH && pl.splits > 1)
-    e = launch(true, head_join_kernel<T>, dim3((s.d + 255) / 256, static_cast<unsigned>(std::min<int64_t>(s.N, 4096))), 256,
-               0, st, static_cast<const HeadState*>(state), reinterpret_cast<const float*>(ws + pl.o_acc), pl.splits,
-               pl.n_pad, pl.ldacc, s.d, static_cast<const int*>(rows), dH);
+  // two passes; after EXP they leave at once unless it asked for them
+  const int retry = pl.one_pass ? 1 : 0;
+  HeadGemm p = logits(0, s.V);
+  p.only_retry = retry;
+  e = run_gemm<STATS, PLANES>(p, mt * p.n_tiles, st);
+  if (e == cudaSuccess) e = losses(false, retry);
+  for (int i = 0; grads && e == cudaSuccess && i < pl.pieces; ++i) {
+    const int v0 = i * pl.piece, cols = std::min(pl.piece, s.V - v0);
+    p = logits(v0, cols);
+    p.only_retry = retry;
+    e = run_gemm<GRAD, PLANES>(p, mt * p.n_tiles, st);
+    if (e == cudaSuccess && s.dH) e = input_grad(i, v0, cols, false, retry);
+    if (e == cudaSuccess && s.dW) {
+      HeadGemm x = base;
+      x.mapA = g_mn;
+      x.mapB = H_mn;
+      x.mapH = X_mn;
+      x.direct = direct ? 2 : 0;
+      x.planeA = pl.piece;
+      x.planeB = pl.plane;
+      x.v0 = v0;
+      x.m_tiles = p.n_tiles;
+      x.n_tiles = dt;
+      x.out = dW;
+      e = run_gemm<DW, PLANES>(x, static_cast<int64_t>(x.m_tiles) * dt, st);
+    }
+  }
   return e;
 }
 

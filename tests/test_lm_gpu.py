@@ -234,6 +234,51 @@ def test_head_infinite_and_large_logits():
     assert got.loss[keep].isfinite().all() and got.dH[keep].isfinite().all()
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_head_input_gradient_in_one_pass(dt):
+    """The gradient of H alone, of a size that takes one pass over the vocabulary, for usual rows and
+    where one row, or every row, has a loss too large for its reference."""
+    H, W, labels, w = head_inputs(520, 512, 40001, dt, outside=0.05)
+    w[3] = 0.0
+    H[3] = math.nan
+    for scale in (None, 5, "all"):
+        if scale == 5:      # one row far from its label: a loss of some hundreds
+            H[7] = (-60.0 * W[labels[7].clamp(min=0)].float()).to(H.dtype)
+        if scale == "all":
+            H = (H.float() * 50.0).to(H.dtype)
+        got = lm.head_loss(H, W, labels, weights=w)
+        r = ref.head(H, W, labels, w)
+        bl, bH, _ = ref.head_bounds(r, H.dtype)
+        print("of the bounds:", float(r["loss"].max()), ref.check(got.loss, r["loss"], bl, "loss"),
+              ref.check(got.dH, r["dH"], bH, "dH"))
+        only = lm.head_loss(H, W, labels, weights=w, grad=False).loss
+        assert torch.allclose(got.loss, only, rtol=2e-5, atol=2e-5)
+
+
+def test_head_one_pass_infinite_logits():
+    H, W, labels, _ = head_inputs(300, 512, 70000, "bf16", weighted=False)
+    H[5] = math.nan                            # the row's own NaN
+    W[69000] = 0.0
+    W[69000, 0] = math.inf                     # logits of +inf or -inf, by the sign of h
+    H[:, 0] = -1.0
+    labels[labels == 69000] = 0
+    got = lm.head_loss(H, W, labels)
+    keep = torch.arange(300, device="cuda") != 5
+    Wf = W.clone()
+    Wf[69000] = 0.0
+    z = H[keep].double() @ Wf.double().T
+    z[:, 69000] = -math.inf
+    want = -torch.log_softmax(z, 1).gather(1, labels[keep][:, None])[:, 0]
+    assert got.loss[5].isnan() and torch.allclose(got.loss[keep].double(), want, rtol=1e-5, atol=1e-5)
+    H[9, 0] = 1.0                              # one row meets +inf: no softmax
+    got = lm.head_loss(H, W, labels)
+    keep[9] = False
+    want = -torch.log_softmax(z, 1).gather(1, labels[torch.arange(300, device="cuda") != 5][:, None])[:, 0]
+    assert got.loss[9].isnan() or float(got.loss[9]) == math.inf
+    sel = keep[torch.arange(300, device="cuda") != 5]
+    assert torch.allclose(got.loss[keep].double(), want[sel], rtol=1e-5, atol=1e-5)
+
+
 def test_head_gradients_against_differences():
     H, W, labels, w = head_inputs(20, 48, 130, "f32")
     got = lm.head_loss(H, W, labels, weights=w, weight_grad=True)
