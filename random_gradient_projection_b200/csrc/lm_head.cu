@@ -46,8 +46,8 @@
 // rounded to nearest, in registers.
 //
 // The kernel: a cluster of two CTAs (one tile of 256 x 256, cta_group::2), each CTA with half of
-// A's rows and half of B's columns in its ring of shared-memory stages.  Warps 17-19 of each
-// CTA load by TMA, warp 16 of CTA 0 issues the MMAs for both, warps 0-15 are the epilogue of their
+// A's rows and half of B's columns in its ring of shared-memory stages.  Warp 17 of each
+// CTA loads by TMA, warp 16 of CTA 0 issues the MMAs for both, warps 0-15 are the epilogue of their
 // CTA's 128 rows (each 32 rows x 64 columns, in registers); two 256-column accumulators in TMEM
 // let it overlap the next sums.
 #include <cuda.h>
@@ -73,9 +73,8 @@ constexpr int kStages = 6;
 constexpr int kStage = 2 * kHalf * kBK * 2;   // A half and B half: 32 KB
 constexpr int kEpiWarps = 16;
 constexpr int kCols = 64;             // columns of an epilogue warp
-constexpr int kMmaWarp = kEpiWarps;   // then the producers: together a fifth warpgroup
-constexpr int kProducers = 3;
-constexpr int kThreads = 32 * (kEpiWarps + 1 + kProducers);
+constexpr int kMmaWarp = kEpiWarps, kLoadWarp = kEpiWarps + 1;   // of a fifth warpgroup
+constexpr int kThreads = 32 * (kEpiWarps + 4);
 // Registers per thread: 640 threads are launched with 96 each (61440); the epilogue's 512 take
 // 112, the other 128 keep 32 (61440 again; without this the epilogues spill).
 constexpr int kRegsLaunch = 96, kRegsEpi = 112, kRegsOther = 32;
@@ -85,7 +84,6 @@ constexpr int kBarOff = kStages * kStage;
 constexpr int kBoxOff = kBarOff + 1024;
 constexpr int kSmem = kBoxOff + kEpiWarps * kBox + 1024;   // + alignment slack
 static_assert(kBoxOff % 1024 == 0, "boxes are aligned");
-static_assert(kProducers <= kStages, "parity waits need at most as many producers as stages");
 static_assert(kSmem <= 227 * 1024, "shared memory of an SM");
 constexpr int kGroupM = 8;            // row tiles that share a column of B tiles in L2
 constexpr uint64_t kWaitLimitNs = 4000000000ull;
@@ -244,7 +242,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t rank = ptx::cluster_ctarank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    return ptx::mbar_wait_or_abort(bar, parity, kWaitLimitNs, abort_flag);
+    return ptx::mbar_wait_suspend_or_abort(bar, parity, kWaitLimitNs, abort_flag);
   };
 
   ptx::griddep_launch_dependents();
@@ -255,7 +253,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     for (int s = 0; s < kStages; ++s) {
-      ptx::mbar_init(&full[s], 2);
+      ptx::mbar_init(&full[s], 1);
       ptx::mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -285,9 +283,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (warp >= kMmaWarp) {
     ptx::setmaxnreg_dec<kRegsOther>();   // the whole warpgroup, one instruction
-    if (warp > kMmaWarp) {
-    // ---------------- TMA producers ----------------
-    const int producer = warp - kMmaWarp - 1;
+    if (warp == kLoadWarp) {
+    // ---------------- TMA producer ----------------
     if (lane == 0) {
       const bool all_live = n_live == p.n_rows;
       const CUtensorMap* mapA = p.direct == 1 && all_live ? &p.mapH : &p.mapA;
@@ -303,7 +300,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           plane_pair(PLANES, prod, &pa, &pb);
           const int ax = pa * p.planeA, bx = pb * p.planeB;
           for (int kb = c.kb0; kb < c.kb1; ++kb, ++it) {
-            if (static_cast<int>(it % kProducers) != producer) continue;
             const int s = it % kStages;
             const uint32_t use = it / kStages;
             if (use > 0 && !wait(&empty[s], (use - 1) & 1)) {
@@ -322,7 +318,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               continue;   // the stage never completes, and the bounded waits end the kernel
             }
 #endif
-            ptx::mbar_arrive_expect_tx_cluster(bar, kStage);
+            // CTA 0 announces the bytes of both (those of CTA 1 may land first: the phase still waits for
+            // this one arrival).  An arrival of CTA 1 on the remote barrier cost 3/4 of the rate.
+            if (rank == 0) ptx::mbar_arrive_expect_tx(&full[s], 2 * kStage);
             if (kAMn) {
               ptx::tma_load_2d_pair(sa, mapA, bar, ax + am, k);
               ptx::tma_load_2d_pair(sa + 8192, mapA, bar, ax + am + 64, k);
@@ -340,10 +338,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
       // Neither CTA may leave while the pair's MMAs still signal its barriers: wait until the
-      // last use of every stage of this producer is released.
+      // last use of every stage is released.
       if (ok && !*abort_flag) {
         for (uint32_t k = it > kStages ? it - kStages : 0; k < it; ++k)
-          if (static_cast<int>(k % kProducers) == producer && !wait(&empty[k % kStages], (k / kStages) & 1)) {
+          if (!wait(&empty[k % kStages], (k / kStages) & 1)) {
             fail(p, kErrTimeout);
             break;
           }
@@ -353,7 +351,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         while (ptx::globaltimer_ns() - t0 < kDrainNs) __nanosleep(1000);
       }
     }
-    } else {
+    } else if (warp == kMmaWarp) {
     // ---------------- UMMA issuer (CTA 0) ----------------
     if (rank == 0 && lane == 0) {
       uint32_t it = 0, ch = 0;   // stage uses, accumulator uses
