@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 #include <nvtx3/nvToolsExt.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <new>
@@ -25,14 +26,25 @@ struct NvtxRange {
   ~NvtxRange() { nvtxRangePop(); }
 };
 
-// The kernels are built for sm_100a only.
+// The kernels are built for sm_100a only.  A device's answer is kept: it cannot change.
 int check_device(bool tensor_maps) {
-  int dev = 0, major = 0, minor = 0;
+  constexpr int kDevices = 64;
+  static std::atomic<int> fits[kDevices];   // 0: not asked yet, 1: yes, 2: no
+  int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
-  if (e != cudaSuccess) return fail_global(GRAPE_ECUDA, std::string("device query: ") + cudaGetErrorString(e));
-  if (major != 10 || minor != 0) return fail_global(GRAPE_EUNSUPPORTED, "needs an sm_100a device (B200)");
+  int known = e == cudaSuccess && dev < kDevices ? fits[dev].load(std::memory_order_relaxed) : 0;
+  if (e == cudaSuccess && known == 0) {
+    int major = 0, minor = 0;
+    e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
+    known = major == 10 && minor == 0 ? 1 : 2;
+    if (e == cudaSuccess && dev < kDevices) fits[dev].store(known, std::memory_order_relaxed);
+  }
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return fail_global(GRAPE_ECUDA, std::string("device query: ") + cudaGetErrorString(e));
+  }
+  if (known != 1) return fail_global(GRAPE_EUNSUPPORTED, "needs an sm_100a device (B200)");
   if (tensor_maps && !grape::tc_tensor_maps_available())
     return fail_global(GRAPE_EUNSUPPORTED, "cuTensorMapEncodeTiled is not available from the driver");
   return GRAPE_OK;

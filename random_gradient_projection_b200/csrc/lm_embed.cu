@@ -135,11 +135,14 @@ __global__ void __launch_bounds__(kLookupThreads) embed_kernel(const TT* __restr
 // ---- order by (token, position) ---------------------------------------------------------------
 // A stable least-significant-digit radix sort of the token numbers by one cluster, whose
 // CTAs exchange their digit counts through distributed shared memory: no launch per pass,
-// and the lists stay in L2.  A warp owns consecutive items, so counting them with
-// match_any in item order makes the placement stable.  Items outside [0, vocab) get the key
+// and the lists stay in L2.  A warp owns consecutive items, so counting them
+// in item order makes the placement stable.  Items outside [0, vocab) get the key
 // `vocab` and so end up last.  Digits have 8 bits at most: two passes up to 65535 tokens.
-// Latency bound: per pass two sweeps of n / (32 warps x CTAs x 32) rounds.
-constexpr int kSortThreads = 1024, kSortWarps = 32, kSortBins = 256, kSortCluster = 8;
+// Up to kSortHeld items a CTA (65536 ids), a pass puts its items in order in shared memory first, so
+// that they are written as runs (scattered 4-byte stores made up half of the kernel); beyond, they
+// are scattered.  Latency bound: a pass is one round trip to L2 and two cluster barriers.
+constexpr int kSortThreads = 1024, kSortWarps = 32, kSortBins = 256, kSortCluster = 8, kSortRounds = 8;
+constexpr int kSortHeld = kSortThreads * kSortRounds;
 
 __device__ __forceinline__ uint32_t ld_dsmem_u32(uint32_t cluster_addr) {
   uint32_t v;
@@ -147,24 +150,40 @@ __device__ __forceinline__ uint32_t ld_dsmem_u32(uint32_t cluster_addr) {
   return v;
 }
 
+// The lanes with this lane's digit (0 .. kSortBins, the last for no item), by one vote per bit.
+__device__ __forceinline__ uint32_t equal_digits(int digit) {
+  uint32_t same = 0xffffffffu;
+#pragma unroll
+  for (int b = 0; b <= 8; ++b) {
+    const bool bit = (digit >> b) & 1;
+    const uint32_t v = __ballot_sync(0xffffffffu, bit);
+    same &= bit ? v : ~v;
+  }
+  return same;
+}
+
 __global__ void __launch_bounds__(kSortThreads) embed_order_kernel(const void* ids, int id_bytes, int n, int vocab,
                                                                    int passes, int digit_bits, int* positions,
                                                                    int* tokens, int* tmp_positions, int* tmp_tokens,
                                                                    uint32_t* present) {
   __shared__ uint32_t cnt[kSortWarps][kSortBins];
-  __shared__ uint32_t tot[kSortBins], base[kSortBins], wsum[kSortBins / 32];
+  __shared__ uint32_t tot[kSortBins], base[kSortBins], lbase[kSortBins], wsum[kSortBins / 32], lsum[kSortBins / 32];
+  extern __shared__ int held[];   // keys, then positions (kSortHeld each)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int ctas = gridDim.x, rank = blockIdx.x;   // the grid is one cluster
   const uint32_t lt = (1u << lane) - 1;
 
   for (int w = rank * kSortThreads + tid; w < (vocab + 31) / 32; w += ctas * kSortThreads) present[w] = 0;
 
-  // this warp's items [w0, w1): whole rounds of 32
+  // this warp's items [w0, w1): whole rounds of 32, kSortRounds of them at a time in registers
   const int64_t per = ((static_cast<int64_t>(n) + ctas * kSortThreads - 1) / (ctas * kSortThreads)) * 32;
   const int64_t first = (static_cast<int64_t>(rank) * kSortWarps + warp) * per;
   const int w0 = static_cast<int>(first < n ? first : n);
   const int w1 = static_cast<int>(first + per < n ? first + per : n);
   const int mask = (1 << digit_bits) - 1;
+  const bool hold = per <= 32 * kSortRounds;   // all of a CTA's items fit
+  const int64_t cta0 = static_cast<int64_t>(rank) * kSortWarps * per;
+  const int mine = static_cast<int>(cta0 >= n ? 0 : min(static_cast<int64_t>(n) - cta0, kSortWarps * per));
 
   for (int p = 0; p < passes; ++p) {
     const int shift = p * digit_bits;
@@ -173,18 +192,61 @@ __global__ void __launch_bounds__(kSortThreads) embed_order_kernel(const void* i
     const int* src_tok = to_final ? tmp_tokens : tokens;
     int* dst_pos = to_final ? positions : tmp_positions;
     int* dst_tok = to_final ? tokens : tmp_tokens;
-    auto key_of = [&](int j) { return p == 0 ? token_at(ids, id_bytes, j, vocab) : __ldcg(src_tok + j); };
+    int key[kSortRounds], pos[kSortRounds];
+    auto load = [&](int j0) {   // all rounds' loads in flight; -1: no item
+      if (p > 0) {
+#pragma unroll
+        for (int k = 0; k < kSortRounds; ++k) {
+          const int j = j0 + 32 * k + lane;
+          key[k] = -1;
+          if (j < w1) {
+            key[k] = __ldcg(src_tok + j);
+            pos[k] = __ldcg(src_pos + j);
+          }
+        }
+        return;
+      }
+      if (id_bytes == 8) {
+        int64_t id[kSortRounds];
+#pragma unroll
+        for (int k = 0; k < kSortRounds; ++k) {
+          const int j = j0 + 32 * k + lane;
+          id[k] = j < w1 ? __ldg(static_cast<const long long*>(ids) + j) : 0;
+        }
+#pragma unroll
+        for (int k = 0; k < kSortRounds; ++k) key[k] = id[k] >= 0 && id[k] < vocab ? static_cast<int>(id[k]) : vocab;
+      } else {
+#pragma unroll
+        for (int k = 0; k < kSortRounds; ++k) {
+          const int j = j0 + 32 * k + lane;
+          key[k] = j < w1 ? __ldg(static_cast<const int*>(ids) + j) : 0;
+        }
+#pragma unroll
+        for (int k = 0; k < kSortRounds; ++k) key[k] = key[k] >= 0 && key[k] < vocab ? key[k] : vocab;
+      }
+#pragma unroll
+      for (int k = 0; k < kSortRounds; ++k) {
+        pos[k] = j0 + 32 * k + lane;
+        if (pos[k] >= w1) key[k] = -1;
+      }
+    };
+    auto digit_of = [&](int k) { return k < 0 ? kSortBins : (k >> shift) & mask; };   // no item: a bin of its own
 
     for (int i = tid; i < kSortWarps * kSortBins; i += kSortThreads) (&cnt[0][0])[i] = 0;
+    if (w0 < w1) load(w0);
     __syncthreads();
-    for (int j0 = w0; j0 < w1; j0 += 32) {
-      const int j = j0 + lane;
-      const bool have = j < w1;
-      const int digit = have ? (key_of(j) >> shift) & mask : kSortBins;   // no item: a bin of its own
-      const uint32_t same = __match_any_sync(0xffffffffu, digit);
-      if (have && (same & lt) == 0) cnt[warp][digit] += __popc(same);
-      __syncwarp();
+    for (int j0 = w0; j0 < w1; j0 += 32 * kSortRounds) {
+      if (j0 > w0) load(j0);
+#pragma unroll
+      for (int k = 0; k < kSortRounds; ++k) {
+        if (j0 + 32 * k >= w1) break;
+        const int digit = digit_of(key[k]);
+        const uint32_t same = equal_digits(digit);
+        if (digit < kSortBins && (same & lt) == 0) cnt[warp][digit] += __popc(same);
+        __syncwarp();
+      }
     }
+    if (!hold && w0 < w1) load(w0);   // the placement starts over (otherwise they are still here)
     __syncthreads();
     if (tid < kSortBins) {   // items of bin `tid` in the warps before each warp
       uint32_t run = 0;
@@ -200,45 +262,79 @@ __global__ void __launch_bounds__(kSortThreads) embed_order_kernel(const void* i
       ptx::cluster_sync();
     else
       __syncthreads();
-    uint32_t before = 0, all = 0;
     if (tid < kSortBins) {
-      for (int c = 0; c < ctas; ++c) {
-        const uint32_t x = ctas > 1 ? ld_dsmem_u32(ptx::cluster_addr(&tot[tid], c)) : tot[tid];
-        before += c < rank ? x : 0;
-        all += x;
+      uint32_t all = 0, before = 0, x[kSortCluster];
+#pragma unroll
+      for (int c = 0; c < kSortCluster; ++c)
+        x[c] = ctas == 1 ? (c == 0 ? tot[tid] : 0) : ld_dsmem_u32(ptx::cluster_addr(&tot[tid], c));
+#pragma unroll
+      for (int c = 0; c < kSortCluster; ++c) {
+        before += c < rank ? x[c] : 0;
+        all += x[c];
       }
-      uint32_t incl = all;   // scan over the bins
+      uint32_t incl = all, lincl = tot[tid];   // scans over the bins: of the cluster, of this CTA
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
+        const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o), z = __shfl_up_sync(0xffffffffu, lincl, o);
+        if (lane >= o) incl += y, lincl += z;
       }
-      if (lane == 31) wsum[warp] = incl;
+      if (lane == 31) wsum[warp] = incl, lsum[warp] = lincl;
       base[tid] = incl - all + before;
+      lbase[tid] = lincl - tot[tid];
     }
     __syncthreads();
     if (tid < kSortBins) {
-      uint32_t add = 0;
-      for (int w = 0; w < warp; ++w) add += wsum[w];
+      uint32_t add = 0, ladd = 0;
+      for (int w = 0; w < warp; ++w) add += wsum[w], ladd += lsum[w];
       base[tid] += add;
+      lbase[tid] += ladd;
     }
     __syncthreads();
-    for (int j0 = w0; j0 < w1; j0 += 32) {
-      const int j = j0 + lane;
-      const bool have = j < w1;
-      const int key = have ? key_of(j) : 0;
-      const int pos = p == 0 ? j : (have ? __ldcg(src_pos + j) : 0);
-      const int digit = have ? (key >> shift) & mask : kSortBins;
-      const uint32_t same = __match_any_sync(0xffffffffu, digit);
-      uint32_t at = 0;
-      if (have) at = base[digit] + cnt[warp][digit] + __popc(same & lt);
-      __syncwarp();
-      if (have) {
-        if ((same & lt) == 0) cnt[warp][digit] += __popc(same);
-        dst_pos[at] = pos;
-        dst_tok[at] = key;
+    if (hold) {
+#pragma unroll
+      for (int k = 0; k < kSortRounds; ++k) {
+        if (w0 + 32 * k >= w1) break;
+        const int digit = digit_of(key[k]);
+        const uint32_t same = equal_digits(digit);
+        uint32_t at = 0;
+        if (digit < kSortBins) at = lbase[digit] + cnt[warp][digit] + __popc(same & lt);
+        __syncwarp();
+        if (digit < kSortBins) {
+          if ((same & lt) == 0) cnt[warp][digit] += __popc(same);
+          held[at] = key[k];
+          held[kSortHeld + at] = pos[k];
+        }
+        __syncwarp();
       }
-      __syncwarp();
+      __syncthreads();
+      for (int i = tid; i < mine; i += kSortThreads) {
+        const int k = held[i], digit = digit_of(k);
+        const uint32_t at = base[digit] + (i - lbase[digit]);
+        dst_pos[at] = held[kSortHeld + i];
+        dst_tok[at] = k;
+        // last pass: these items are in the order of their whole keys now
+        if (p == passes - 1 && k < vocab && (i == 0 || held[i - 1] != k)) atomicOr(present + (k >> 5), 1u << (k & 31));
+      }
+      __syncthreads();   // `held` and the counts may be written again
+    } else {
+      for (int j0 = w0; j0 < w1; j0 += 32 * kSortRounds) {
+        if (j0 > w0) load(j0);
+#pragma unroll
+        for (int k = 0; k < kSortRounds; ++k) {
+          if (j0 + 32 * k >= w1) break;
+          const int digit = digit_of(key[k]);
+          const uint32_t same = equal_digits(digit);
+          uint32_t at = 0;
+          if (digit < kSortBins) at = base[digit] + cnt[warp][digit] + __popc(same & lt);
+          __syncwarp();
+          if (digit < kSortBins) {
+            if ((same & lt) == 0) cnt[warp][digit] += __popc(same);
+            dst_pos[at] = pos[k];
+            dst_tok[at] = key[k];
+          }
+          __syncwarp();
+        }
+      }
     }
     // the lists are read by other threads (and CTAs) next
     __threadfence();
@@ -248,6 +344,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_order_kernel(const void* i
       __syncthreads();
   }
   // which tokens occur at all: their rows of the gradient are written by the sums, the others zeroed
+  if (hold) return;
   for (int j = rank * kSortThreads + tid; j < n; j += ctas * kSortThreads) {
     const int t = __ldcg(tokens + j);
     if (t < vocab && (j == 0 || __ldcg(tokens + j - 1) != t)) atomicOr(present + (t >> 5), 1u << (t & 31));
@@ -426,92 +523,131 @@ __global__ void __launch_bounds__(32 * kSegWarps) segment_kernel(const SegParams
   if (NORMS && lane < len) p.slots[static_cast<size_t>(tile) * p.n + pos] = slot;
 }
 
-// The runs that begin in a chunk and go on in the next ones: the warp of the chunk where a run
-// begins adds its partial sums in chunk order.
+// The runs that begin in a chunk and go on in the next ones: their partial sums, added in a fixed
+// order.  A CTA looks at eight chunks, one per warp, in one 256-column tile.  A run over few chunks is
+// added by its warp; a longer one by all eight warps, an eighth of its chunks each.
+constexpr int kJoinWarps = 8, kJoinAlone = 16;
+
+__device__ __forceinline__ void add_parts(const SegParams& p, int c0, int c1, int tile, int lane, float (&acc)[8]) {
+#pragma unroll 1
+  for (int c = c0; c < c1; c += 4) {   // four in flight
+    float4 a[4], b[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (c + u < c1) {
+        const float4* q = reinterpret_cast<const float4*>(part_at(p, c + u, 0, tile, lane));
+        a[u] = __ldcg(q);
+        b[u] = __ldcg(q + 1);
+      }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (c + u < c1) {
+        acc[0] += a[u].x, acc[1] += a[u].y, acc[2] += a[u].z, acc[3] += a[u].w;
+        acc[4] += b[u].x, acc[5] += b[u].y, acc[6] += b[u].z, acc[7] += b[u].w;
+      }
+  }
+}
+
 template <bool VEC, bool NORMS>
-__global__ void __launch_bounds__(32 * kSegWarps) segment_join_kernel(const SegParams p) {
+__global__ void __launch_bounds__(32 * kJoinWarps) segment_join_kernel(const SegParams p) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
+  __shared__ int long_more[kJoinWarps];
+  __shared__ float sums[kJoinWarps][256];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t job = static_cast<int64_t>(blockIdx.x) * kSegWarps + warp;
-  const int chunk = static_cast<int>(job / p.tiles), tile = static_cast<int>(job % p.tiles);
-  if (chunk >= p.chunks) return;
-  const int c0 = chunk * p.R, c1 = c0 + p.R;
-  if (c1 >= p.n) return;
-  const int t = __ldg(p.tokens + c1 - 1);
-  const int sample = NORMS ? __ldg(p.positions + c1 - 1) / p.T : 0;
+  const int first = blockIdx.x / p.tiles * kJoinWarps, tile = blockIdx.x % p.tiles;
+  const int chunk = first + warp, c0 = chunk * p.R, c1 = c0 + p.R;
+  // does a run begin in this chunk and go on, and through how many chunks after it?
+  int t = p.vocab, sample = 0, more = 0;
   auto same = [&](int j) {
     return __ldg(p.tokens + j) == t && (!NORMS || __ldg(p.positions + j) / p.T == sample);
   };
-  if (t >= p.vocab || !same(c1)) return;
-  if (same(c0) && c0 > 0 && same(c0 - 1)) return;   // it began earlier
-  // chunks after this one that the run reaches: all but the last of them are full of it
-  int more = 1;
-  while (true) {
-    const int64_t e = static_cast<int64_t>(chunk + more + lane + 1) * p.R;   // end of the (more + lane)-th chunk after
-    const bool on = e < p.n && same(static_cast<int>(e) - 1) && same(static_cast<int>(e));
-    const uint32_t m = __ballot_sync(0xffffffffu, on);
-    if (m == 0xffffffffu) {
-      more += 32;
-      continue;
+  if (chunk < p.chunks && c1 < p.n) {
+    t = __ldg(p.tokens + c1 - 1);
+    if (NORMS) sample = __ldg(p.positions + c1 - 1) / p.T;
+    if (t < p.vocab && same(c1) && !(same(c0) && c0 > 0 && same(c0 - 1))) {
+      more = 1;   // all but the last of these chunks are full of the run
+      while (true) {
+        const int64_t e = static_cast<int64_t>(chunk + more + lane + 1) * p.R;   // end of the chunk `more + lane` after
+        const bool on = e < p.n && same(static_cast<int>(e) - 1) && same(static_cast<int>(e));
+        const uint32_t m = __ballot_sync(0xffffffffu, on);
+        more += m == 0xffffffffu ? 32 : __ffs(~m) - 1;
+        if (m != 0xffffffffu) break;
+      }
     }
-    more += __ffs(~m) - 1;
-    break;
   }
-  float acc[8];
-  auto part = [&](int c, int which, float (&v)[8]) {
-    const float4* q = reinterpret_cast<const float4*>(part_at(p, c, which, tile, lane));
-    const float4 a = __ldcg(q), b = __ldcg(q + 1);
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  if (lane == 0) long_more[warp] = more > kJoinAlone ? more : 0;
+  __syncthreads();
+
+  auto finish = [&](float (&acc)[8]) {   // by the run's warp
+    if (NORMS) {
+      float ss = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss = fmaf(acc[i], acc[i], ss);
+      ss = warp_sum(ss);
+      // the run's first item in this chunk
+      const uint32_t m = __ballot_sync(0xffffffffu, lane < p.R && same(c0 + lane));   // a suffix of the chunk's lanes
+      if (lane == 0) p.slots[static_cast<size_t>(tile) * p.n + __ldg(p.positions + c0 + __ffs(m) - 1)] = ss;
+    } else {
+      store_grad<VEC>(p, t, lane_col<VEC>(tile, lane), acc);
+    }
   };
-  part(chunk, 1, acc);
-  int k = 1;
-  for (; k + 3 <= more; k += 4) {
-    float v[4][8];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) part(chunk + k + u, 0, v[u]);
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] += v[u][i];
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  auto begin = [&]() {
+    const float4* q = reinterpret_cast<const float4*>(part_at(p, chunk, 1, tile, lane));
+    const float4 a = __ldcg(q), b = __ldcg(q + 1);
+    acc[0] = a.x, acc[1] = a.y, acc[2] = a.z, acc[3] = a.w, acc[4] = b.x, acc[5] = b.y, acc[6] = b.z, acc[7] = b.w;
+  };
+  if (more > 0 && more <= kJoinAlone) {
+    begin();
+    add_parts(p, chunk + 1, chunk + 1 + more, tile, lane, acc);
+    finish(acc);
   }
-  for (; k <= more; ++k) {
-    float v[8];
-    part(chunk + k, 0, v);
+  for (int k = 0; k < kJoinWarps; ++k) {   // the long ones, one after another
+    const int n = long_more[k];
+    if (n == 0) continue;
+    const int from = first + k + 1;
+    float part[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    add_parts(p, from + static_cast<int>(static_cast<int64_t>(n) * warp / kJoinWarps),
+              from + static_cast<int>(static_cast<int64_t>(n) * (warp + 1) / kJoinWarps), tile, lane, part);
+    store8(&sums[warp][lane * 8], part);
+    __syncthreads();
+    if (warp == k) {
+      begin();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] += v[i];
-  }
-  if (NORMS) {
-    float ss = 0.0f;
+      for (int w = 0; w < kJoinWarps; ++w)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(acc[i], acc[i], ss);
-    ss = warp_sum(ss);
-    // the run's first item in this chunk
-    const bool in = lane < p.R && same(c0 + lane);
-    const uint32_t m = __ballot_sync(0xffffffffu, in);   // a suffix of the chunk's lanes
-    if (lane == 0) p.slots[static_cast<size_t>(tile) * p.n + __ldg(p.positions + c0 + __ffs(m) - 1)] = ss;
-  } else {
-    store_grad<VEC>(p, t, lane_col<VEC>(tile, lane), acc);
+        for (int i = 0; i < 8; ++i) acc[i] += sums[w][lane * 8 + i];
+      finish(acc);
+    }
+    __syncthreads();
   }
 }
 
 // sq[b] = sum of the slots of sample b over all tiles, in a fixed order.
-__global__ void __launch_bounds__(256) sample_sums_kernel(const float* slots, int n, int T, int tiles, float* sq) {
+constexpr int kSumThreads = 1024;
+__global__ void __launch_bounds__(kSumThreads) sample_sums_kernel(const float* slots, int n, int T, int tiles, float* sq) {
   ptx::griddep_wait();
-  __shared__ float red[8];
+  __shared__ float red[kSumThreads / 32];
   float s = 0.0f;
-  for (int tile = 0; tile < tiles; ++tile) {
-    const float* q = slots + static_cast<size_t>(tile) * n + static_cast<size_t>(blockIdx.x) * T;
-    for (int t = threadIdx.x; t < T; t += 256) s += q[t];
+  const float* q = slots + static_cast<size_t>(blockIdx.x) * T;
+  const int64_t total = static_cast<int64_t>(T) * tiles;
+  for (int64_t i0 = threadIdx.x; i0 < total; i0 += 8 * kSumThreads) {   // eight in flight
+    float x[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int64_t i = i0 + u * kSumThreads;
+      x[u] = i < total ? __ldcg(q + i / T * n + i % T) : 0.0f;
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) s += x[u];
   }
   s = warp_sum(s);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    float tot = 0.0f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) tot += red[k];
-    sq[blockIdx.x] = tot;
+  if (threadIdx.x < 32) {
+    s = warp_sum(red[threadIdx.x]);
+    if (threadIdx.x == 0) sq[blockIdx.x] = s;
   }
 }
 
@@ -556,14 +692,18 @@ SegParams seg_params(const void* order, int B, int T, int vocab, int d, float sc
   return p;
 }
 
+unsigned join_blocks(const SegParams& p) {
+  return static_cast<unsigned>((p.chunks + kJoinWarps - 1) / kJoinWarps) * static_cast<unsigned>(p.tiles);
+}
+
 template <class TG, bool VEC>
 cudaError_t run_sqnorms(const SegParams& p, int B, const TG* G, float* sq, cudaStream_t st) {
   const int64_t jobs = static_cast<int64_t>(p.chunks) * p.tiles;
   const unsigned blocks = static_cast<unsigned>((jobs + kSegWarps - 1) / kSegWarps);
   cudaError_t e = launch(false, segment_kernel<TG, VEC, true>, blocks, 32 * kSegWarps, st, p, G);
-  if (e == cudaSuccess) e = launch(true, segment_join_kernel<VEC, true>, blocks, 32 * kSegWarps, st, p);
+  if (e == cudaSuccess) e = launch(true, segment_join_kernel<VEC, true>, join_blocks(p), 32 * kJoinWarps, st, p);
   if (e == cudaSuccess)
-    e = launch(true, sample_sums_kernel, B, 256, st, static_cast<const float*>(p.slots), p.n, p.T, p.tiles, sq);
+    e = launch(true, sample_sums_kernel, B, kSumThreads, st, static_cast<const float*>(p.slots), p.n, p.T, p.tiles, sq);
   return e;
 }
 
@@ -575,7 +715,7 @@ cudaError_t run_grad(SegParams p, const TG* G, cudaStream_t st) {
   p.seg_blocks = static_cast<int>(blocks);
   cudaError_t e = launch(false, segment_kernel<TG, VEC, false>, blocks + zero, 32 * kSegWarps, st, p, G);
   if (e == cudaSuccess && blocks > 0)
-    e = launch(true, segment_join_kernel<VEC, false>, blocks, 32 * kSegWarps, st, p);
+    e = launch(true, segment_join_kernel<VEC, false>, join_blocks(p), 32 * kJoinWarps, st, p);
   return e;
 }
 
@@ -615,10 +755,14 @@ cudaError_t embed_order(const void* ids, int id_bytes, int64_t n, int vocab, voi
   int bits = 1;
   while (vocab >> bits) ++bits;   // keys 0 .. vocab
   const int passes = (bits + 7) / 8, digit_bits = (bits + passes - 1) / passes;
+  const int smem = 2 * kSortHeld * 4;
+  cudaError_t e = tc_configure_kernel(reinterpret_cast<const void*>(embed_order_kernel), smem, kSortThreads);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   const int ctas = n > 2048 ? kSortCluster : 1;
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kSortThreads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute a[1];
   a[0].id = cudaLaunchAttributeClusterDimension;

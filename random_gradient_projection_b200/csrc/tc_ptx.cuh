@@ -104,6 +104,26 @@ __device__ __forceinline__ bool mbar_wait_suspend_or_abort(uint64_t* bar, uint32
   }
 }
 
+// As mbar_wait_or_abort, sleeping `pause_ns` between tries: for warps that share an SM with busy
+// ones and are not in a hurry.
+__device__ __forceinline__ bool mbar_wait_pause_or_abort(uint64_t* bar, uint32_t parity, uint64_t limit_ns,
+                                                         volatile int* abort, uint32_t pause_ns) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i) {
+      __nanosleep(pause_ns);
+      if (mbar_try_wait(bar, parity)) return true;
+    }
+    if (*abort) return false;
+    if (globaltimer_ns() - t0 > limit_ns) {
+      *abort = 1;
+      return false;
+    }
+  }
+}
+
 // ---- TMA: tiled loads into this CTA's own shared memory, and tiled stores ----------
 __device__ __forceinline__ void prefetch_tmap(const CUtensorMap* m) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
@@ -187,6 +207,18 @@ __device__ __forceinline__ void bulk_wait_group0() {
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// Untiled bulk copies (both addresses 16-byte aligned, size a multiple of 16).
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
+               : "memory");
 }
 
 // Make this thread's generic-proxy writes to shared memory visible to the async
@@ -289,6 +321,13 @@ __device__ __forceinline__ void umma_commit(uint64_t* bar) {
       "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
           smem_u32(bar))
       : "memory");
+}
+
+// Maximum over the warp (NaN ignored unless all are).
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // ---- registers per thread, changed by a whole warpgroup (four consecutive warps) ---------

@@ -130,10 +130,10 @@ def lib() -> ctypes.CDLL:
 
 def _ptr(x) -> int:
     """Address of a torch tensor, an int, or None (0)."""
-    if x is None:
-        return 0
     if isinstance(x, int):
         return x
+    if x is None:
+        return 0
     if hasattr(x, "data_ptr"):
         return x.data_ptr()
     if isinstance(x, np.ndarray):

@@ -12,17 +12,21 @@ different streams share nothing.
 """
 from __future__ import annotations
 
-import contextlib
 from typing import NamedTuple, Optional
 
 from . import grape
 from .grape import GRAPE_BF16, GRAPE_F32
 
+try:
+    import torch
+except ImportError:   # the package itself does not need it
+    torch = None
+
 
 class HeadLoss(NamedTuple):
-    loss: "torch.Tensor"            # noqa: F821  per row, weighted
-    dH: Optional["torch.Tensor"]    # noqa: F821
-    dW: Optional["torch.Tensor"]    # noqa: F821
+    loss: "torch.Tensor"            # per row, weighted
+    dH: Optional["torch.Tensor"]
+    dW: Optional["torch.Tensor"]
 
 
 class EmbedOrder:
@@ -32,7 +36,6 @@ class EmbedOrder:
         self.B, self.T, self.vocab, self.buffer = B, T, vocab, buffer
 
     def _list(self, k: int):
-        import torch
         n = self.B * self.T
         start = k * ((n * 4 + 255) // 256 * 256)
         return self.buffer[start:start + 4 * n].view(torch.int32)
@@ -48,54 +51,57 @@ class EmbedOrder:
         return self._list(1)
 
 
+# ---- checks, of every tensor and before any address is passed on --------------------------
+
 def _dtype(x, what: str) -> int:
-    import torch
-    t = getattr(x, "dtype", None)
-    if t == torch.float32:
+    t = x.dtype
+    if t is torch.float32:
         return GRAPE_F32
-    if t == torch.bfloat16:
+    if t is torch.bfloat16:
         return GRAPE_BF16
-    raise ValueError(f"{what}: need a float32 or bfloat16 tensor, got {t or type(x).__name__}")
+    raise ValueError(f"{what}: need a float32 or bfloat16 tensor, got {t}")
 
 
-def _tensor(x, what: str, shape=None, dtypes=None):
-    """A contiguous CUDA tensor on the current device, of this shape (None: any size there)."""
-    import torch
+def _tensor(x, what: str, dev: int, shape=None, dtypes=None):
+    """A contiguous CUDA tensor on device `dev` (the current one), of this shape (None: any size)."""
     if not isinstance(x, torch.Tensor):
         raise ValueError(f"{what}: need a torch tensor, got {type(x).__name__}")
     if dtypes is not None and x.dtype not in dtypes:
         raise ValueError(f"{what}: need one of {[str(t) for t in dtypes]}, got {x.dtype}")
-    if shape is not None and (x.dim() != len(shape) or any(s is not None and s != g for s, g in zip(shape, x.shape))):
-        raise ValueError(f"{what}: need shape {tuple('any' if s is None else s for s in shape)}, got {tuple(x.shape)}")
+    if shape is not None:
+        got = x.shape
+        ok = len(got) == len(shape)
+        if ok:
+            for want, size in zip(shape, got):
+                if want is not None and want != size:
+                    ok = False
+        if not ok:
+            raise ValueError(f"{what}: need shape {tuple('any' if s is None else s for s in shape)}, got {tuple(got)}")
     if not x.is_contiguous():
         raise ValueError(f"{what}: need a contiguous tensor, got strides {x.stride()}")
-    if not x.is_cuda or x.device.index != torch.cuda.current_device():
+    if x.get_device() != dev or not x.is_cuda:
         raise ValueError(f"{what}: need a tensor on the current CUDA device, got one on {x.device}")
     return x
 
 
-def _ids(x, what: str, shape=None) -> int:
-    import torch
-    _tensor(x, what, shape, (torch.int32, torch.int64))
-    return x.element_size()
+def _ids(x, what: str, dev: int, shape=None) -> int:
+    _tensor(x, what, dev, shape, (torch.int32, torch.int64))
+    return 4 if x.dtype is torch.int32 else 8
 
 
-def _weights(x, n: int, what: str = "weights"):
-    import torch
-    if x is not None:
-        _tensor(x, what, (n,), (torch.float32,))
-
-
-def _out(x, shape, dtype, what: str):
-    """`x` checked, or a new tensor (on the stream that is current)."""
-    import torch
+def _weights(x, dev: int, shape):
+    """Address of the weights (0: none)."""
     if x is None:
-        return torch.empty(shape, dtype=dtype, device="cuda")
-    return _tensor(x, what, shape, (dtype,))
+        return 0
+    return _tensor(x, "weights", dev, shape, (torch.float32,)).data_ptr()
+
+
+def _out(x, shape, dtype, dev: int, like):
+    """`x` checked, or a new tensor beside `like` (on the stream that is current)."""
+    return like.new_empty(shape, dtype=dtype) if x is None else _tensor(x, "out", dev, shape, (dtype,))
 
 
 def _torch_dtype(dtype):
-    import torch
     if dtype in ("bf16", GRAPE_BF16, torch.bfloat16):
         return torch.bfloat16
     if dtype in ("f32", GRAPE_F32, torch.float32):
@@ -103,54 +109,64 @@ def _torch_dtype(dtype):
     raise ValueError(f"dtype: need 'bf16' or 'f32', got {dtype!r}")
 
 
-@contextlib.contextmanager
-def _on(stream):
-    """Makes `stream` (None: the current one) current, so that what is allocated belongs to it,
-    and yields its handle."""
-    import torch
-    if stream is None:
-        yield torch.cuda.current_stream().cuda_stream
-        return
-    handle = stream if isinstance(stream, int) else stream.cuda_stream
-    with torch.cuda.stream(torch.cuda.ExternalStream(handle)):
-        yield handle
+class _On:
+    """Makes `stream` (None: the current one) current, so that what is allocated belongs to it;
+    entering gives its handle."""
+
+    def __init__(self, stream):
+        self.stream, self.inner = stream, None
+
+    def __enter__(self):
+        if self.stream is None:
+            return torch.cuda.current_stream().cuda_stream
+        handle = self.stream if isinstance(self.stream, int) else self.stream.cuda_stream
+        self.inner = torch.cuda.stream(torch.cuda.ExternalStream(handle))
+        self.inner.__enter__()
+        return handle
+
+    def __exit__(self, *exc):
+        if self.inner is not None:
+            self.inner.__exit__(*exc)
 
 
-def _bytes(n: int):
-    import torch
-    return torch.empty(max(int(n), 1), dtype=torch.uint8, device="cuda")
+def _scratch(n: int, like):
+    return like.new_empty((max(n, 1),), dtype=torch.uint8)
 
+
+# ---- embedding -----------------------------------------------------------------------------
 
 def embed(table, ids, scale: float = 1.0, dtype="bf16", out=None, stream=None):
     """``scale * table[ids]`` in ``dtype``: ids of any shape, rows of ids outside the table zero."""
-    _tensor(table, "table", (None, None))
+    dev = torch.cuda.current_device()
+    _tensor(table, "table", dev, (None, None))
     tdt = _dtype(table, "table")
-    id_bytes = _ids(ids, "ids")
+    id_bytes = _ids(ids, "ids", dev)
     V, d = table.shape
     if V < 1 or d < 1:
         raise ValueError(f"table: need at least one row and one column, got {tuple(table.shape)}")
     odt = _torch_dtype(dtype)
-    with _on(stream) as st:
-        out = _out(out, (*ids.shape, d), odt, "out")
-        grape.grape_embed(table, tdt, ids, id_bytes, ids.numel(), V, d, float(scale), _dtype(out, "out"), out, st)
+    with _On(stream) as st:
+        out = _out(out, (*ids.shape, d), odt, dev, table)
+        grape.grape_embed(table.data_ptr(), tdt, ids.data_ptr(), id_bytes, ids.numel(), V, d, scale,
+                          GRAPE_F32 if odt is torch.float32 else GRAPE_BF16, out.data_ptr(), st)
     return out
 
 
 def embed_order(ids, vocab: int, stream=None) -> EmbedOrder:
     """The order of a batch's ids (B x T), for ``embed_sqnorms`` and ``embed_grad``."""
-    id_bytes = _ids(ids, "ids", (None, None))
+    id_bytes = _ids(ids, "ids", torch.cuda.current_device(), (None, None))
     B, T = ids.shape
-    n = grape.grape_embed_order_bytes(B * T, int(vocab))
-    with _on(stream) as st:
-        order = EmbedOrder(B, T, int(vocab), _bytes(n))
-        grape.grape_embed_order(ids, id_bytes, B * T, order.vocab, order.buffer, st)
+    vocab = int(vocab)
+    n = grape.grape_embed_order_bytes(B * T, vocab)
+    with _On(stream) as st:
+        order = EmbedOrder(B, T, vocab, _scratch(n, ids))
+        grape.grape_embed_order(ids.data_ptr(), id_bytes, B * T, vocab, order.buffer.data_ptr(), st)
     return order
 
 
-def _embed_args(order: EmbedOrder, Gout):
-    import torch
-    _tensor(Gout, "Gout", (order.B, order.T, None))
-    _tensor(order.buffer, "order", None, (torch.uint8,))
+def _embed_args(order: EmbedOrder, Gout, dev: int):
+    _tensor(Gout, "Gout", dev, (order.B, order.T, None))
+    _tensor(order.buffer, "order", dev)
     d = Gout.shape[2]
     if d < 1:
         raise ValueError(f"Gout: need at least one column, got {tuple(Gout.shape)}")
@@ -159,26 +175,30 @@ def _embed_args(order: EmbedOrder, Gout):
 
 def embed_sqnorms(order: EmbedOrder, Gout, scale: float = 1.0, out=None, stream=None):
     """Each sample's squared norm of the embedding table's gradient (B floats)."""
-    import torch
-    dt, d, n = _embed_args(order, Gout)
-    with _on(stream) as st:
-        out = _out(out, (order.B,), torch.float32, "out")
-        grape.grape_embed_sqnorms(order.buffer, order.B, order.T, order.vocab, d, Gout, dt, float(scale), _bytes(n),
-                                  out, st)
+    dev = torch.cuda.current_device()
+    dt, d, n = _embed_args(order, Gout, dev)
+    with _On(stream) as st:
+        out = _out(out, (order.B,), torch.float32, dev, Gout)
+        ws = _scratch(n, Gout)
+        grape.grape_embed_sqnorms(order.buffer.data_ptr(), order.B, order.T, order.vocab, d, Gout.data_ptr(), dt, scale,
+                                  ws.data_ptr(), out.data_ptr(), st)
     return out
 
 
 def embed_grad(order: EmbedOrder, Gout, weights=None, scale: float = 1.0, out=None, stream=None):
     """The embedding table's gradient (vocab x d, fp32), every sample's share times its weight."""
-    import torch
-    dt, d, n = _embed_args(order, Gout)
-    _weights(weights, order.B)
-    with _on(stream) as st:
-        out = _out(out, (order.vocab, d), torch.float32, "out")
-        grape.grape_embed_grad(order.buffer, order.B, order.T, order.vocab, d, Gout, dt, float(scale), weights,
-                               _bytes(n), out, st)
+    dev = torch.cuda.current_device()
+    dt, d, n = _embed_args(order, Gout, dev)
+    w = _weights(weights, dev, (order.B,))
+    with _On(stream) as st:
+        out = _out(out, (order.vocab, d), torch.float32, dev, Gout)
+        ws = _scratch(n, Gout)
+        grape.grape_embed_grad(order.buffer.data_ptr(), order.B, order.T, order.vocab, d, Gout.data_ptr(), dt, scale, w,
+                               ws.data_ptr(), out.data_ptr(), st)
     return out
 
+
+# ---- losses --------------------------------------------------------------------------------
 
 def head_loss(H, W, labels, weights=None, grad: bool = True, weight_grad: bool = False, stream=None) -> HeadLoss:
     """Softmax cross entropy of the head ``H @ W.T`` without its logits: losses, and on request
@@ -186,24 +206,25 @@ def head_loss(H, W, labels, weights=None, grad: bool = True, weight_grad: bool =
 
     H is N x d or B x T x d, labels N or B x T; a label outside the vocabulary, or weight 0,
     drops the token."""
-    import torch
-    if not isinstance(H, torch.Tensor) or H.dim() not in (2, 3):
-        raise ValueError("H: need a tensor of 2 or 3 dimensions")
-    _tensor(H, "H")
+    dev = torch.cuda.current_device()
+    _tensor(H, "H", dev)
+    if H.dim() not in (2, 3):
+        raise ValueError(f"H: need 2 or 3 dimensions, got {tuple(H.shape)}")
     dt = _dtype(H, "H")
     rows, d = H.shape[:-1], H.shape[-1]
-    N = H.numel() // d if d else 0
-    _tensor(W, "W", (None, d), (H.dtype,))
+    _tensor(W, "W", dev, (None, d), (H.dtype,))
     V = W.shape[0]
-    id_bytes = _ids(labels, "labels", rows)
-    if weights is not None:
-        _tensor(weights, "weights", rows, (torch.float32,))
-    n = grape.grape_head_loss_bytes(N, d, V, dt, bool(grad), bool(weight_grad))
-    with _on(stream) as st:
-        loss = torch.empty(rows, dtype=torch.float32, device="cuda")
+    id_bytes = _ids(labels, "labels", dev, rows)
+    w = _weights(weights, dev, rows)
+    N = labels.numel()
+    n = grape.grape_head_loss_bytes(N, d, V, dt, grad, weight_grad)
+    with _On(stream) as st:
+        loss = H.new_empty(rows, dtype=torch.float32)
         dH = torch.empty_like(H) if grad else None
         dW = torch.empty_like(W) if weight_grad else None
-        grape.grape_head_loss(H, W, labels, id_bytes, weights, N, d, V, dt, _bytes(n), loss, dH, dW, st)
+        ws = _scratch(n, H)
+        grape.grape_head_loss(H.data_ptr(), W.data_ptr(), labels.data_ptr(), id_bytes, w, N, d, V, dt, ws.data_ptr(),
+                              loss.data_ptr(), dH.data_ptr() if grad else 0, dW.data_ptr() if weight_grad else 0, st)
     return HeadLoss(loss, dH, dW)
 
 
@@ -212,27 +233,26 @@ def distill_loss(logits, indices, values, weights=None, temperature: float = 1.0
     numbers ``indices`` (..., K), a negative index for an absent entry.
 
     ``out`` may be ``logits`` itself: Gout then replaces them."""
-    import torch
-    if not isinstance(logits, torch.Tensor) or logits.dim() not in (2, 3):
-        raise ValueError("logits: need a tensor of 2 or 3 dimensions")
-    _tensor(logits, "logits")
+    dev = torch.cuda.current_device()
+    _tensor(logits, "logits", dev)
+    if logits.dim() not in (2, 3):
+        raise ValueError(f"logits: need 2 or 3 dimensions, got {tuple(logits.shape)}")
     dt = _dtype(logits, "logits")
     rows, V = logits.shape[:-1], logits.shape[-1]
-    id_bytes = _ids(indices, "indices", (*rows, None))
+    id_bytes = _ids(indices, "indices", dev, (*rows, None))
     K = indices.shape[-1]
-    _tensor(values, "values", (*rows, K))
+    _tensor(values, "values", dev, (*rows, K))
     vdt = _dtype(values, "values")
-    if weights is not None:
-        _tensor(weights, "weights", rows, (torch.float32,))
+    w = _weights(weights, dev, rows)
     if out is not None:
-        _tensor(out, "out", logits.shape, (logits.dtype,))
+        _tensor(out, "out", dev, logits.shape, (logits.dtype,))
         a, b, size = logits.data_ptr(), out.data_ptr(), logits.numel() * logits.element_size()
         if a != b and abs(a - b) < size:
             raise ValueError("out: may be the logits themselves, but not overlap them in part")
-    N = logits.numel() // V if V else 0
-    with _on(stream) as st:
-        out = torch.empty_like(logits) if out is None else out
-        loss = torch.empty(rows, dtype=torch.float32, device="cuda")
-        grape.grape_distill_loss(logits, dt, N, V, indices, id_bytes, values, vdt, K, weights, float(temperature),
-                                 loss, out, st)
+    with _On(stream) as st:
+        if out is None:
+            out = torch.empty_like(logits)
+        loss = logits.new_empty(rows, dtype=torch.float32)
+        grape.grape_distill_loss(logits.data_ptr(), dt, loss.numel(), V, indices.data_ptr(), id_bytes,
+                                 values.data_ptr(), vdt, K, w, temperature, loss.data_ptr(), out.data_ptr(), st)
     return loss, out
