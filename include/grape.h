@@ -214,6 +214,22 @@ GRAPE_API int grape_set_graph(grape_ctx* ctx, int32_t enable);
 enum grape_norm_method { GRAPE_NORM_DIRECT = 0, GRAPE_NORM_GHOST = 1 };
 GRAPE_API int grape_set_norm_method(grape_ctx* ctx, int32_t method);
 
+/* Parameters beside the stack: their share of each sample's norm, and the clip factors for their
+ * sums.  Clipping takes a sample's norm over all its parameters ("Metodologia: DP-GRAPE",
+ * design choice 2, technical summary of "Memory-Efficient Differentially Private Training with
+ * Gradient Random Projection"), so a parameter whose gradient the caller forms, such as an
+ * embedding table (grape_embed_sqnorms), adds its squared norm before the clip and its sum
+ * takes the same c_i (grape_embed_grad).
+ * grape_set_extra_sqnorms: the device address of B floats that every following step and
+ *   accumulation adds to its n_i^2 (read when the step's work runs, so a caller refills the
+ *   buffer for each step, in stream order); NULL (the default) adds nothing.  Graphs captured
+ *   with another address are dropped.  grape_sqnorms is not affected.
+ * grape_clip_ptr: device address of the B clip factors c_i of the last step or accumulation
+ *   (library-owned, rewritten by the next one).
+ * Errors: GRAPE_EINVAL (NULL ctx or clip_dev, misaligned address). */
+GRAPE_API int grape_set_extra_sqnorms(grape_ctx* ctx, const float* sqnorms_dev);
+GRAPE_API int grape_clip_ptr(grape_ctx* ctx, float** clip_dev);
+
 /* How S_l = sum_i c_i R_{i,l} is formed (the aggregation of the clipped projected
  * per-sample gradients in the closing paragraph of "Metodologia: DP-GRAPE", technical
  * summary of "Memory-Efficient Differentially Private Training with Gradient Random

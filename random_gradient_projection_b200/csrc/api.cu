@@ -866,6 +866,24 @@ int grape_set_graph(grape_ctx* ctx, int32_t enable) {
   return GRAPE_OK;
 }
 
+int grape_set_extra_sqnorms(grape_ctx* ctx, const float* sqnorms_dev) {
+  if (!ctx) return set_global(GRAPE_EINVAL, "ctx must not be null");
+  if (reinterpret_cast<uintptr_t>(sqnorms_dev) & 3u)
+    return ctx->fail(GRAPE_EINVAL, "sqnorms_dev must be aligned to its element size");
+  if (sqnorms_dev != ctx->sh.extra_sq) {   // captured graphs hold the other address
+    for (auto& g : ctx->graphs) ctx->drop_graph(g);
+    ctx->graphs.clear();
+  }
+  ctx->sh.extra_sq = sqnorms_dev;
+  return GRAPE_OK;
+}
+
+int grape_clip_ptr(grape_ctx* ctx, float** clip_dev) {
+  if (!ctx || !clip_dev) return set_global(GRAPE_EINVAL, "ctx and clip_dev must not be null");
+  *clip_dev = ctx->clip;
+  return GRAPE_OK;
+}
+
 int grape_set_norm_method(grape_ctx* ctx, int32_t method) {
   if (!ctx) return set_global(GRAPE_EINVAL, "ctx must not be null");
   if (method != GRAPE_NORM_DIRECT && method != GRAPE_NORM_GHOST)

@@ -40,6 +40,7 @@ struct StepShape {
   float lr, beta1, beta2, eps;
   float one_minus_beta1, one_minus_beta2;
   int part_stride;         // norm-partial slots per sample over all layers
+  const float* extra_sq;   // per sample, added to the layers' squared norm before the clip; null: none
 };
 
 // Per-step scalars of the update.

@@ -85,6 +85,7 @@ constexpr int kBoxOff = kBarOff + 1024;
 constexpr int kSmem = kBoxOff + kEpiWarps * kBox + 1024;   // + alignment slack
 static_assert(kBoxOff % 1024 == 0, "boxes are aligned");
 static_assert(kSmem <= 227 * 1024, "shared memory of an SM");
+constexpr int kSplitBlocks = 24;      // (a block takes about 0.1 us, joining the splits 3)
 constexpr int kGroupM = 8;            // row tiles that share a column of B tiles in L2
 constexpr uint64_t kWaitLimitNs = 4000000000ull;
 constexpr uint64_t kDrainNs = 20000000ull;
@@ -902,11 +903,11 @@ struct HeadPlan {
     piece = static_cast<int>(((vmax + pieces - 1) / pieces + kTile - 1) / kTile * kTile);
     pieces = static_cast<int>((vmax + piece - 1) / piece);
     // few tiles of dH: its long sum over the vocabulary is split over the CTA pairs, at least
-    // eight blocks of 64 each
+    // kSplitBlocks blocks of 64 each
     const int64_t out_tiles = n_pad / kTile * ((s.d + kTile - 1) / kTile);
     splits = 1;
     if (s.dH && pieces == 1 && out_tiles > 0 && out_tiles < 74)
-      splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(74 / out_tiles, piece / kBK / 8)));
+      splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(74 / out_tiles, piece / kBK / kSplitBlocks)));
     acc = s.dH && (pieces > 1 || splits > 1);
     ldacc = (s.d + 3) / 4 * 4;
     size_t o = 256;

@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kThreads) clip_kernel(StepShape sh, const floa
   for (int k = threadIdx.x; k < sh.part_stride; k += kThreads) ss += p[k];
   const float tot = block_sum(ss);
   if (threadIdx.x == 0) {
-    const float n = sqrtf(tot);
+    const float n = sqrtf(sh.extra_sq ? tot + sh.extra_sq[i] : tot);
     norms[i] = n;
     clip[i] = (n > sh.C) ? sh.C / n : 1.0f;
   }

@@ -1982,8 +1982,8 @@ struct ApTable {
 };
 
 __global__ void __launch_bounds__(256) clip_scale_kernel(ApTable t, int r, int T, int part_stride, float C,
-                                                         const float* partials, float* norms, float* clip,
-                                                         int rescale) {
+                                                         const float* partials, const float* extra_sq,
+                                                         float* norms, float* clip, int rescale) {
   __shared__ float red[8];
   __shared__ float c_sh;
   ptx::griddep_launch_dependents();
@@ -1999,7 +1999,7 @@ __global__ void __launch_bounds__(256) clip_scale_kernel(ApTable t, int r, int T
   if (threadIdx.x == 0) {
     float tot = 0.0f;
     for (int w = 0; w < 8; ++w) tot += red[w];
-    const float n = sqrtf(tot);
+    const float n = sqrtf(extra_sq ? tot + extra_sq[i] : tot);
     const float c = (n > C) ? C / n : 1.0f;
     if (l == 0) {
       norms[i] = n;
@@ -2898,7 +2898,7 @@ cudaError_t tc_clip_scale(const StepShape& sh, const LayerWs* ws, const TcWorksp
   for (int l = 0; l < sh.L; ++l) t.AP[l] = static_cast<__nv_bfloat16*>(ws[l].AP);
   ++*launches;
   return launch_pdl(clip_scale_kernel, dim3(sh.B, rescale_ap ? sh.L : 1), dim3(256), 0, st, t, sh.r, sh.T,
-                    sh.part_stride, sh.C, partials, norms, clip, rescale_ap ? 1 : 0);
+                    sh.part_stride, sh.C, partials, sh.extra_sq, norms, clip, rescale_ap ? 1 : 0);
 }
 
 cudaError_t tc_aggregate_stored(const StepShape& sh, const LayerWs* ws, const float* clip, cudaStream_t st,

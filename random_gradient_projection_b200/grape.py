@@ -37,7 +37,7 @@ EXPORTS = (
     "grape_set_aggregation", "grape_aggregation_of",
     "grape_embed", "grape_embed_order_bytes", "grape_embed_order", "grape_embed_workspace_bytes",
     "grape_embed_sqnorms", "grape_embed_grad", "grape_head_loss_bytes", "grape_head_loss",
-    "grape_distill_loss",
+    "grape_distill_loss", "grape_set_extra_sqnorms", "grape_clip_ptr",
 )
 GRAPE_NORM_DIRECT, GRAPE_NORM_GHOST = 0, 1
 GRAPE_AGG_AUTO, GRAPE_AGG_RECOMPUTE, GRAPE_AGG_STORE = 0, 1, 2
@@ -109,6 +109,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "grape_embed_grad": ([vp, i32, i32, i32, i32, vp, i32, f64, vp, vp, vp, vp], i32),
         "grape_head_loss_bytes": ([i64, i32, i32, i32, i32, i32, ctypes.POINTER(u64)], i32),
         "grape_head_loss": ([vp, vp, vp, i32, vp, i64, i32, i32, i32, vp, vp, vp, vp, vp], i32),
+        "grape_set_extra_sqnorms": ([vp, vp], i32),
+        "grape_clip_ptr": ([vp, ctypes.POINTER(vp)], i32),
         "grape_distill_loss": ([vp, i32, i64, i32, vp, i32, vp, i32, i32, vp, f64, vp, vp, vp], i32),
     }
     for name, (args, res) in sig.items():
@@ -329,6 +331,16 @@ def grape_gaussian(seed: int, layer: int, step: int, stream_id: int, n: int, out
                                 _stream(stream)))
 
 
+def grape_set_extra_sqnorms(ctx: int, sqnorms_dev):
+    _check(lib().grape_set_extra_sqnorms(ctx, _ptr(sqnorms_dev)), ctx)
+
+
+def grape_clip_ptr(ctx: int) -> int:
+    out = ctypes.c_void_p()
+    _check(lib().grape_clip_ptr(ctx, ctypes.byref(out)), ctx)
+    return out.value
+
+
 def grape_embed(table, table_dtype: int, ids, id_bytes: int, n_ids: int, vocab: int, d: int, scale: float,
                 out_dtype: int, out, stream=None):
     _check(lib().grape_embed(_ptr(table), table_dtype, _ptr(ids), id_bytes, n_ids, vocab, d, scale,
@@ -456,6 +468,19 @@ class GrapeStep:
     def set_norm_method(self, method: int):
         """GRAPE_NORM_DIRECT (default) or GRAPE_NORM_GHOST (tensor-core path)."""
         grape_set_norm_method(self.ctx, method)
+
+    def set_extra_sqnorms(self, sqnorms):
+        """Squared norms (B floats on the device, or None) of parameters beside the stack, which
+        every following step adds to its samples' before the clip.  The tensor is kept
+        referenced and read when a step runs."""
+        _need(sqnorms, self.B * 4, 4, "sqnorms", True)
+        grape_set_extra_sqnorms(self.ctx, sqnorms)
+        self._extra_sqnorms = sqnorms
+
+    def clip_tensor(self):
+        """The clip factors c_i of the last step as a torch tensor sharing the library's memory."""
+        import torch
+        return torch.as_tensor(_DeviceArray(grape_clip_ptr(self.ctx), (self.B,)), device="cuda")
 
     def set_aggregation(self, method: int):
         """GRAPE_AGG_AUTO (the default), GRAPE_AGG_RECOMPUTE or GRAPE_AGG_STORE."""

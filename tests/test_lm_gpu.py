@@ -120,11 +120,32 @@ def test_distill(N, V, K, dt, tau):
     ref.check(loss1, rl, bl, "loss"), ref.check(G1, rG, bG, "Gout")
 
 
-def test_distill_masked_rows_and_infinities():
-    logits, idx, val, w = distill_inputs(8, 5000, 6, "bf16", absent=0.0)
+@pytest.mark.parametrize("N,V,K,dt", [
+    (700, 20001, 40, "bf16"), (700, 16385, 64, "bf16"), (400, 60001, 100, "f32"), (500, 33000, 128, "f32"),
+    (330, 110003, 9, "bf16"), (900, 9001, 130, "f32"), (320, 20001, 129, "bf16")])
+def test_distill_many_rows_per_block(N, V, K, dt):
+    """Several rows in turn on every SM, some of them without weight or teacher; in place too."""
+    logits, idx, val, w = distill_inputs(N, V, K, dt)
+    w[::5] = 0.0
+    w[7:40] = 0.0
+    logits[w == 0] = math.nan
+    idx[3::11] = -1
+    loss, G = lm.distill_loss(logits, idx, val, weights=w, temperature=1.3)
+    for a in range(0, N, 100):
+        rl, rG, bl, bG = ref.distill(logits[a:a + 100], idx[a:a + 100], val[a:a + 100], w[a:a + 100], 1.3)
+        ref.check(loss[a:a + 100], rl, bl, "loss"), ref.check(G[a:a + 100], rG, bG, "Gout")
+    for _ in range(3):
+        inplace = logits.clone()
+        again = lm.distill_loss(inplace, idx, val, weights=w, temperature=1.3, out=inplace)
+        assert torch.equal(again[0], loss) and torch.equal(inplace, G)
+
+
+@pytest.mark.parametrize("V", [5000, 40001])
+def test_distill_masked_rows_and_infinities(V):
+    logits, idx, val, w = distill_inputs(8, V, 6, "bf16", absent=0.0)
     w[1] = 0.0
     logits[1] = math.nan                      # no weight: not read
-    idx[2] = torch.tensor([-1, 5000, -9, 6000, -1, -2], device="cuda")
+    idx[2] = torch.tensor([-1, V, -9, V + 1000, -1, -2], device="cuda")
     logits[2] = math.inf                      # no valid entry
     logits[3, 10:4000] = -math.inf            # a masked vocabulary
     idx[3] = torch.arange(6, device="cuda")
@@ -141,11 +162,21 @@ def test_distill_masked_rows_and_infinities():
     assert loss[6].isnan() and G[6].isnan().all() and G[[0, 3, 4, 5, 7]].isfinite().all()
 
 
-def test_distill_the_same_index_twice():
-    logits, _, val, _ = distill_inputs(4, 300, 5, "f32")
-    idx = torch.tensor([[3, 3, 7, 3, 7], [0, 299, 0, 1, 2], [5, 5, 5, 5, 5], [9, -1, 9, 300, 9]], device="cuda")
+@pytest.mark.parametrize("V", [300, 30000])
+def test_distill_the_same_index_twice(V):
+    logits, _, val, _ = distill_inputs(4, V, 5, "f32")
+    idx = torch.tensor([[3, 3, 7, 3, 7], [0, V - 1, 0, 1, 2], [5, 5, 5, 5, 5], [9, -1, 9, V, 9]], device="cuda")
     loss, G = lm.distill_loss(logits, idx, val)
     rl, rG, bl, bG = ref.distill(logits, idx, val, None, 1.0)
+    ref.check(loss, rl, bl, "loss"), ref.check(G, rG, bG, "Gout")
+
+
+def test_distill_the_same_index_in_several_warps():
+    logits, idx, val, w = distill_inputs(300, 40000, 100, "bf16", absent=0.1)
+    idx[:, 70:] = idx[:, :30]                 # every index again, far behind its first place
+    idx[5] = 17
+    loss, G = lm.distill_loss(logits, idx, val, weights=w)
+    rl, rG, bl, bG = ref.distill(logits, idx, val, w, 1.0)
     ref.check(loss, rl, bl, "loss"), ref.check(G, rG, bG, "Gout")
 
 
