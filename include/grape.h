@@ -474,8 +474,8 @@ GRAPE_API int grape_embed_grad(const void* order, int32_t B, int32_t T, int32_t 
  *  weights    N floats (a token's share of its sample's loss, a clip factor), NULL for 1
  *  loss       N floats
  *  dH, dW     N x d and vocab x d in dtype, or NULL: not computed
- *  workspace  grape_head_loss_bytes bytes: the live rows of H, 8 N vocab / 128 bytes of partial
- *             sums, one piece of the logits' gradient (at most 128 MiB, or 4096 columns for a
+ *  workspace  grape_head_loss_bytes bytes: the live rows of H, 8 N vocab / 256 bytes of partial
+ *             sums, one piece of the logits' gradient (at most 256 MiB, or 4096 columns for a
  *             large N), for fp32 or d % 8 != 0 a laid-out copy of W, and fp32 sums of dH where it
  *             is summed in pieces
  * All sums are fp32; with bf16 inputs the logits' gradient is rounded to bf16 before the second

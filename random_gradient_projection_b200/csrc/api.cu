@@ -70,6 +70,7 @@ struct grape_ctx {
   uint32_t refresh = 1;
   int64_t p_key = -1;
   int norm_method = GRAPE_NORM_DIRECT;
+  const float* extra_sq = nullptr;   // caller-owned (grape_set_extra_sqnorms)
   // aggregation (grape_set_aggregation): recompute (diag(c) AP)^T Gout, or sum the R_i the
   // norm kernel stored; agg is never AUTO.  The stored R_i live in the arena when AUTO
   // chose them at create, else in rst_buf, allocated when a caller asks for them.
@@ -289,9 +290,14 @@ int run_accumulate(grape_ctx* ctx, const void* const* A, const void* const* G, i
   int rc = run_project_norm(ctx, io.data(), step, st, stored);
   if (rc) return rc;
   rc = phase(ctx, GRAPE_PHASE_CLIP, "clip", st, [&](int* n) {
+    if (ctx->extra_sq) {
+      const cudaError_t e = grape::add_extra_sqnorms(sh, ctx->extra_sq, ctx->partials, st);
+      if (e != cudaSuccess) return e;
+      ++*n;
+    }
     if (ctx->path == GRAPE_PATH_TC)
       return grape::tc_clip_scale(sh, ws, ctx->tc, ctx->partials, ctx->norms, ctx->clip, !stored, st, n);
-    *n = 1;
+    ++*n;
     return grape::finalize_clip(sh, ctx->partials, ctx->norms, ctx->clip, st);
   });
   if (rc) return rc;
@@ -870,11 +876,11 @@ int grape_set_extra_sqnorms(grape_ctx* ctx, const float* sqnorms_dev) {
   if (!ctx) return set_global(GRAPE_EINVAL, "ctx must not be null");
   if (reinterpret_cast<uintptr_t>(sqnorms_dev) & 3u)
     return ctx->fail(GRAPE_EINVAL, "sqnorms_dev must be aligned to its element size");
-  if (sqnorms_dev != ctx->sh.extra_sq) {   // captured graphs hold the other address
+  if (sqnorms_dev != ctx->extra_sq) {   // captured graphs hold the other address
     for (auto& g : ctx->graphs) ctx->drop_graph(g);
     ctx->graphs.clear();
   }
-  ctx->sh.extra_sq = sqnorms_dev;
+  ctx->extra_sq = sqnorms_dev;
   return GRAPE_OK;
 }
 

@@ -40,7 +40,6 @@ struct StepShape {
   float lr, beta1, beta2, eps;
   float one_minus_beta1, one_minus_beta2;
   int part_stride;         // norm-partial slots per sample over all layers
-  const float* extra_sq;   // per sample, added to the layers' squared norm before the clip; null: none
 };
 
 // Per-step scalars of the update.
@@ -69,6 +68,8 @@ cudaError_t simt_generate_P_set_node(cudaGraphExec_t exec, cudaGraphNode_t node,
                                      const LayerWs* ws, uint32_t key);
 // Per-sample squared norms: each sample's partial slots summed in a fixed order (no clip).
 cudaError_t sum_partials(const StepShape& sh, const float* partials, float* sqnorms, cudaStream_t st);
+// Adds extra[i] to sample i's squared norm (its first partial slot), before the clip.
+cudaError_t add_extra_sqnorms(const StepShape& sh, const float* extra, float* partials, cudaStream_t st);
 cudaError_t finalize_clip(const StepShape& sh, const float* partials, float* norms, float* clip,
                           cudaStream_t st);
 cudaError_t simt_aggregate(const StepShape& sh, const LayerWs* ws, const LayerIo* io,

@@ -22,8 +22,8 @@
 #include <type_traits>
 
 #include "lm.h"
-#include "tc.h"
-#include "tc_ptx.cuh"
+#include "lm_launch.h"
+#include "lm_ptx.cuh"
 
 namespace grape {
 namespace {
@@ -770,9 +770,9 @@ cudaError_t run(const DistillParams& p, const void* logits, void* Gout, cudaStre
 template <class T, int MINB>
 cudaError_t run_rows(const DistillParams& p, const void* logits, void* Gout, cudaStream_t st) {
   const int smem = RowRing<MINB>::kSlots * kChunkBytes;
-  cudaError_t e = tc_configure_kernel(reinterpret_cast<const void*>(distill_rows_kernel<T, MINB>), smem, kRowBlock);
+  cudaError_t e = lm_configure_kernel(reinterpret_cast<const void*>(distill_rows_kernel<T, MINB>), smem);
   if (e != cudaSuccess) return e;
-  const int64_t grid = std::min<int64_t>(p.N, static_cast<int64_t>(MINB) * tc_sm_count());
+  const int64_t grid = std::min<int64_t>(p.N, static_cast<int64_t>(MINB) * lm_sm_count());
   distill_rows_kernel<T, MINB><<<static_cast<unsigned>(grid), kRowBlock, smem, st>>>(
       p, static_cast<const T*>(logits), static_cast<T*>(Gout));
   return cudaGetLastError();

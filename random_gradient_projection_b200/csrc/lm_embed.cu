@@ -21,8 +21,8 @@
 #include <cstdint>
 
 #include "lm.h"
-#include "tc.h"
-#include "tc_ptx.cuh"
+#include "lm_launch.h"
+#include "lm_ptx.cuh"
 
 namespace grape {
 namespace {
@@ -651,20 +651,6 @@ __global__ void __launch_bounds__(kSumThreads) sample_sums_kernel(const float* s
   }
 }
 
-template <class Kern, class... Args>
-cudaError_t launch(bool pdl, Kern kernel, unsigned grid, unsigned block, cudaStream_t st, Args... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(block);
-  cfg.stream = st;
-  cudaLaunchAttribute a[1];
-  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  a[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = a;
-  cfg.numAttrs = pdl ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 int tiles_of(int d) { return (d + 255) / 256; }
 
 // Items per chunk: 32 (a lane each) once that gives every SM 16 warps, else 8, so that a short
@@ -700,10 +686,12 @@ template <class TG, bool VEC>
 cudaError_t run_sqnorms(const SegParams& p, int B, const TG* G, float* sq, cudaStream_t st) {
   const int64_t jobs = static_cast<int64_t>(p.chunks) * p.tiles;
   const unsigned blocks = static_cast<unsigned>((jobs + kSegWarps - 1) / kSegWarps);
-  cudaError_t e = launch(false, segment_kernel<TG, VEC, true>, blocks, 32 * kSegWarps, st, p, G);
-  if (e == cudaSuccess) e = launch(true, segment_join_kernel<VEC, true>, join_blocks(p), 32 * kJoinWarps, st, p);
+  cudaError_t e = lm_launch(false, segment_kernel<TG, VEC, true>, dim3(blocks), 32 * kSegWarps, 0, st, p, G);
   if (e == cudaSuccess)
-    e = launch(true, sample_sums_kernel, B, kSumThreads, st, static_cast<const float*>(p.slots), p.n, p.T, p.tiles, sq);
+    e = lm_launch(true, segment_join_kernel<VEC, true>, dim3(join_blocks(p)), 32 * kJoinWarps, 0, st, p);
+  if (e == cudaSuccess)
+    e = lm_launch(true, sample_sums_kernel, dim3(B), kSumThreads, 0, st, static_cast<const float*>(p.slots), p.n, p.T,
+                  p.tiles, sq);
   return e;
 }
 
@@ -713,9 +701,9 @@ cudaError_t run_grad(SegParams p, const TG* G, cudaStream_t st) {
   const unsigned blocks = static_cast<unsigned>((jobs + kSegWarps - 1) / kSegWarps);
   const unsigned zero = static_cast<unsigned>(std::min<int64_t>((p.vocab + kSegWarps - 1) / kSegWarps, 148 * 8));
   p.seg_blocks = static_cast<int>(blocks);
-  cudaError_t e = launch(false, segment_kernel<TG, VEC, false>, blocks + zero, 32 * kSegWarps, st, p, G);
+  cudaError_t e = lm_launch(false, segment_kernel<TG, VEC, false>, dim3(blocks + zero), 32 * kSegWarps, 0, st, p, G);
   if (e == cudaSuccess && blocks > 0)
-    e = launch(true, segment_join_kernel<VEC, false>, join_blocks(p), 32 * kJoinWarps, st, p);
+    e = lm_launch(true, segment_join_kernel<VEC, false>, dim3(join_blocks(p)), 32 * kJoinWarps, 0, st, p);
   return e;
 }
 
@@ -756,7 +744,7 @@ cudaError_t embed_order(const void* ids, int id_bytes, int64_t n, int vocab, voi
   while (vocab >> bits) ++bits;   // keys 0 .. vocab
   const int passes = (bits + 7) / 8, digit_bits = (bits + passes - 1) / passes;
   const int smem = 2 * kSortHeld * 4;
-  cudaError_t e = tc_configure_kernel(reinterpret_cast<const void*>(embed_order_kernel), smem, kSortThreads);
+  cudaError_t e = lm_configure_kernel(reinterpret_cast<const void*>(embed_order_kernel), smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   const int ctas = n > 2048 ? kSortCluster : 1;

@@ -60,8 +60,8 @@
 #include <cstring>
 
 #include "lm.h"
-#include "tc.h"
-#include "tc_ptx.cuh"
+#include "lm_launch.h"
+#include "lm_ptx.cuh"
 
 namespace grape {
 namespace {
@@ -285,117 +285,117 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp >= kMmaWarp) {
     ptx::setmaxnreg_dec<kRegsOther>();   // the whole warpgroup, one instruction
     if (warp == kLoadWarp) {
-    // ---------------- TMA producer ----------------
-    if (lane == 0) {
-      const bool all_live = n_live == p.n_rows;
-      const CUtensorMap* mapA = p.direct == 1 && all_live ? &p.mapH : &p.mapA;
-      const CUtensorMap* mapB = p.direct == 2 && all_live ? &p.mapH : &p.mapB;
-      uint32_t it = 0;
-      bool ok = true;
-      for (int t = pair; ok && t < tiles; t += pairs) {
-        const Tile c = tile_at(t, mt, p.n_tiles, p.splits, kblocks);
-        const int am = c.m * kTile + static_cast<int>(rank) * kHalf;
-        const int bn = c.n * kTile + static_cast<int>(rank) * kHalf;
-        for (int prod = 0; ok && prod < kProds; ++prod) {
-          int pa, pb;
-          plane_pair(PLANES, prod, &pa, &pb);
-          const int ax = pa * p.planeA, bx = pb * p.planeB;
-          for (int kb = c.kb0; kb < c.kb1; ++kb, ++it) {
-            const int s = it % kStages;
-            const uint32_t use = it / kStages;
-            if (use > 0 && !wait(&empty[s], (use - 1) & 1)) {
-              fail(p, kErrTimeout);
-              ok = false;
-              break;
-            }
-            uint8_t* sa = smem + s * kStage;
-            uint8_t* sb = sa + kStage / 2;
-            const int k = kb * kBK;
-            const uint32_t bar = ptx::cluster_addr(&full[s], 0);
+      // ---------------- TMA producer ----------------
+      if (lane == 0) {
+        const bool all_live = n_live == p.n_rows;
+        const CUtensorMap* mapA = p.direct == 1 && all_live ? &p.mapH : &p.mapA;
+        const CUtensorMap* mapB = p.direct == 2 && all_live ? &p.mapH : &p.mapB;
+        uint32_t it = 0;
+        bool ok = true;
+        for (int t = pair; ok && t < tiles; t += pairs) {
+          const Tile c = tile_at(t, mt, p.n_tiles, p.splits, kblocks);
+          const int am = c.m * kTile + static_cast<int>(rank) * kHalf;
+          const int bn = c.n * kTile + static_cast<int>(rank) * kHalf;
+          for (int prod = 0; ok && prod < kProds; ++prod) {
+            int pa, pb;
+            plane_pair(PLANES, prod, &pa, &pb);
+            const int ax = pa * p.planeA, bx = pb * p.planeB;
+            for (int kb = c.kb0; kb < c.kb1; ++kb, ++it) {
+              const int s = it % kStages;
+              const uint32_t use = it / kStages;
+              if (use > 0 && !wait(&empty[s], (use - 1) & 1)) {
+                fail(p, kErrTimeout);
+                ok = false;
+                break;
+              }
+              uint8_t* sa = smem + s * kStage;
+              uint8_t* sb = sa + kStage / 2;
+              const int k = kb * kBK;
+              const uint32_t bar = ptx::cluster_addr(&full[s], 0);
 #ifdef GRAPE_CHECKED
-            const int xa = kAMn ? ax + am : ax + k, xb = kBMn ? bx + bn : bx + k;
-            if (xa < 0 || xb < 0 || xa % 8 || xb % 8 || k < 0 || am < 0 || bn < 0) {
-              atomicOr(&p.state->err, kErrBounds);
-              continue;   // the stage never completes, and the bounded waits end the kernel
-            }
+              const int xa = kAMn ? ax + am : ax + k, xb = kBMn ? bx + bn : bx + k;
+              if (xa < 0 || xb < 0 || xa % 8 || xb % 8 || k < 0 || am < 0 || bn < 0) {
+                atomicOr(&p.state->err, kErrBounds);
+                continue;   // the stage never completes, and the bounded waits end the kernel
+              }
 #endif
-            // CTA 0 announces the bytes of both (those of CTA 1 may land first: the phase still waits for
-            // this one arrival).  An arrival of CTA 1 on the remote barrier cost 3/4 of the rate.
-            if (rank == 0) ptx::mbar_arrive_expect_tx(&full[s], 2 * kStage);
-            if (kAMn) {
-              ptx::tma_load_2d_pair(sa, mapA, bar, ax + am, k);
-              ptx::tma_load_2d_pair(sa + 8192, mapA, bar, ax + am + 64, k);
-            } else {
-              ptx::tma_load_2d_pair(sa, mapA, bar, ax + k, am);
-            }
-            if (kBMn) {
-              const int y = EPI == DH ? p.v0 + k : k;
-              ptx::tma_load_2d_pair(sb, mapB, bar, bx + bn, y);
-              ptx::tma_load_2d_pair(sb + 8192, mapB, bar, bx + bn + 64, y);
-            } else {
-              ptx::tma_load_2d_pair(sb, mapB, bar, bx + k, p.v0 + bn);
+              // CTA 0 announces the bytes of both (those of CTA 1 may land first: the phase still waits for
+              // this one arrival).  An arrival of CTA 1 on the remote barrier cost 3/4 of the rate.
+              if (rank == 0) ptx::mbar_arrive_expect_tx(&full[s], 2 * kStage);
+              if (kAMn) {
+                ptx::tma_load_2d_pair(sa, mapA, bar, ax + am, k);
+                ptx::tma_load_2d_pair(sa + 8192, mapA, bar, ax + am + 64, k);
+              } else {
+                ptx::tma_load_2d_pair(sa, mapA, bar, ax + k, am);
+              }
+              if (kBMn) {
+                const int y = EPI == DH ? p.v0 + k : k;
+                ptx::tma_load_2d_pair(sb, mapB, bar, bx + bn, y);
+                ptx::tma_load_2d_pair(sb + 8192, mapB, bar, bx + bn + 64, y);
+              } else {
+                ptx::tma_load_2d_pair(sb, mapB, bar, bx + k, p.v0 + bn);
+              }
             }
           }
         }
+        // Neither CTA may leave while the pair's MMAs still signal its barriers: wait until the
+        // last use of every stage is released.
+        if (ok && !*abort_flag) {
+          for (uint32_t k = it > kStages ? it - kStages : 0; k < it; ++k)
+            if (!wait(&empty[k % kStages], (k / kStages) & 1)) {
+              fail(p, kErrTimeout);
+              break;
+            }
+        }
+        if (*abort_flag) {   // let loads in flight land before the CTA leaves
+          const uint64_t t0 = ptx::globaltimer_ns();
+          while (ptx::globaltimer_ns() - t0 < kDrainNs) __nanosleep(1000);
+        }
       }
-      // Neither CTA may leave while the pair's MMAs still signal its barriers: wait until the
-      // last use of every stage is released.
-      if (ok && !*abort_flag) {
-        for (uint32_t k = it > kStages ? it - kStages : 0; k < it; ++k)
-          if (!wait(&empty[k % kStages], (k / kStages) & 1)) {
-            fail(p, kErrTimeout);
-            break;
-          }
-      }
-      if (*abort_flag) {   // let loads in flight land before the CTA leaves
-        const uint64_t t0 = ptx::globaltimer_ns();
-        while (ptx::globaltimer_ns() - t0 < kDrainNs) __nanosleep(1000);
-      }
-    }
     } else if (warp == kMmaWarp) {
-    // ---------------- UMMA issuer (CTA 0) ----------------
-    if (rank == 0 && lane == 0) {
-      uint32_t it = 0, ch = 0;   // stage uses, accumulator uses
-      bool ok = true;
-      for (int t = pair; ok && t < tiles; t += pairs) {
-        const Tile c = tile_at(t, mt, p.n_tiles, p.splits, kblocks);
-        const int steps = kProds * (c.kb1 - c.kb0);
-        int i = 0;
-        do {
-          const int b = ch & 1;
-          const uint32_t use = ch >> 1;
-          if (use > 0 && !wait(&accempty[b], (use - 1) & 1)) {
-            fail(p, kErrTimeout);
-            ok = false;
-            break;
-          }
-          ptx::tc_fence_after();
-          const uint32_t dacc = tmem + b * kTile;
-          const int i0 = i, i1 = steps - i > kChunk ? i + kChunk : steps;
-          for (; i < i1; ++i, ++it) {
-            const int s = it % kStages;
-            if (!wait(&full[s], (it / kStages) & 1)) {
+      // ---------------- UMMA issuer (CTA 0) ----------------
+      if (rank == 0 && lane == 0) {
+        uint32_t it = 0, ch = 0;   // stage uses, accumulator uses
+        bool ok = true;
+        for (int t = pair; ok && t < tiles; t += pairs) {
+          const Tile c = tile_at(t, mt, p.n_tiles, p.splits, kblocks);
+          const int steps = kProds * (c.kb1 - c.kb0);
+          int i = 0;
+          do {
+            const int b = ch & 1;
+            const uint32_t use = ch >> 1;
+            if (use > 0 && !wait(&accempty[b], (use - 1) & 1)) {
               fail(p, kErrTimeout);
               ok = false;
               break;
             }
             ptx::tc_fence_after();
-            const uint32_t a_base = ptx::smem_u32(smem + s * kStage), b_base = a_base + kStage / 2;
+            const uint32_t dacc = tmem + b * kTile;
+            const int i0 = i, i1 = steps - i > kChunk ? i + kChunk : steps;
+            for (; i < i1; ++i, ++it) {
+              const int s = it % kStages;
+              if (!wait(&full[s], (it / kStages) & 1)) {
+                fail(p, kErrTimeout);
+                ok = false;
+                break;
+              }
+              ptx::tc_fence_after();
+              const uint32_t a_base = ptx::smem_u32(smem + s * kStage), b_base = a_base + kStage / 2;
 #pragma unroll
-            for (int k = 0; k < kBK / 16; ++k) {
-              const uint64_t ad = kAMn ? ptx::desc_sw128(a_base + k * 2048, 8192, 1024)
-                                       : ptx::desc_sw128(a_base + k * 32, 16, 1024);
-              const uint64_t bd = kBMn ? ptx::desc_sw128(b_base + k * 2048, 8192, 1024)
-                                       : ptx::desc_sw128(b_base + k * 32, 16, 1024);
-              ptx::umma_bf16_pair(dacc, ad, bd, kIdesc, (i > i0 || k > 0) ? 1u : 0u);
+              for (int k = 0; k < kBK / 16; ++k) {
+                const uint64_t ad = kAMn ? ptx::desc_sw128(a_base + k * 2048, 8192, 1024)
+                                         : ptx::desc_sw128(a_base + k * 32, 16, 1024);
+                const uint64_t bd = kBMn ? ptx::desc_sw128(b_base + k * 2048, 8192, 1024)
+                                         : ptx::desc_sw128(b_base + k * 32, 16, 1024);
+                ptx::umma_bf16_pair(dacc, ad, bd, kIdesc, (i > i0 || k > 0) ? 1u : 0u);
+              }
+              ptx::umma_commit_pair(&empty[s]);
             }
-            ptx::umma_commit_pair(&empty[s]);
-          }
-          ptx::umma_commit_pair(&accfull[b]);
-          ++ch;
-        } while (ok && i < steps);
+            ptx::umma_commit_pair(&accfull[b]);
+            ++ch;
+          } while (ok && i < steps);
+        }
       }
-    }
     }
   } else {
     // ---------------- epilogue: warps 0..15 ----------------
@@ -403,10 +403,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     ptx::setmaxnreg_inc<kRegsEpi>();
     const int q = warp & 3, h = warp >> 2;
     uint8_t* box = smem + kBoxOff + warp * kBox;
-    // this lane's two values in the box of the warp with this lane quarter and columns h2
-    auto part_of = [&](int h2) {
-      return reinterpret_cast<float2*>(smem + kBoxOff + (4 * h2 + q) * kBox) + lane;
+    // this lane's two values in the box of the warp with this lane quarter and columns h2 (STATS, which
+    // stages nothing in the boxes, has two places in turn)
+    auto part_of = [&](int h2, uint32_t turn) {
+      return reinterpret_cast<float2*>(smem + kBoxOff + (4 * h2 + q) * kBox) + lane + (EPI == STATS ? 32 * (turn & 1) : 0);
     };
+    uint32_t turn = 0;
     uint32_t ch = 0;
     auto release = [&]() {   // this accumulator may be overwritten
       ptx::tc_fence_before();
@@ -434,12 +436,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ptx::tc_fence_after();
         if (kStream) break;
         const uint32_t tbase = tmem + (static_cast<uint32_t>(q * 32) << 16) + b * kTile + h * kCols;
+        if (i == 0) {
+          ptx::tmem_ld64(tbase, v);
+        } else {
 #pragma unroll
-        for (int cc = 0; cc < kCols; cc += 8) {
-          float x[8];
-          ptx::tmem_ld8(tbase + cc, x);
+          for (int cc = 0; cc < kCols; cc += 8) {
+            float x[8];
+            ptx::tmem_ld8(tbase + cc, x);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[cc + j] = i == 0 ? x[j] : v[cc + j] + x[j];
+            for (int j = 0; j < 8; ++j) v[cc + j] += x[j];
+          }
         }
         release();
         i = steps - i > kChunk ? i + kChunk : steps;
@@ -476,6 +482,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < kCols; ++j)
               if (label == col0 + j) {
+                // (the reference is this logit up to rounding: far off it, nothing below would hold)
+                if (!(fabsf(v[j] - r) < 60.0f)) atomicOr(&p.state->retry, 1);
                 p.target[row] = v[j] - r;
                 v[j] = -INFINITY;   // left out of the sums
               }
@@ -533,12 +541,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (EPI != GRAD) {
           // the row's four parts, one per warp of its lane quarter, joined in order
           __syncwarp();   // the box has been read out
-          *part_of(h) = part;
+          *part_of(h, turn) = part;
           epi_bar();
           if (h == 0 && live) {
             float2 x[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) x[k] = *part_of(k);
+            for (int k = 0; k < 4; ++k) x[k] = *part_of(k, turn);
             float2 y;
             if (EPI == EXP) {
               y = make_float2(((x[0].x + x[1].x) + x[2].x) + x[3].x, 0.0f);
@@ -552,7 +560,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             p.parts[static_cast<int64_t>(p.v0 / kTile + c.n) * p.n_pad + row] = y;
           }
-          epi_bar();   // the boxes may be written again
+          if (EPI != STATS) epi_bar();   // the boxes may be written again
+          ++turn;
         }
       } else {   // DH, DW: 16 columns at a time through the box
         using T = typename HeadType<PLANES>::T;
@@ -872,9 +881,10 @@ __global__ void __launch_bounds__(256) head_join_kernel(const HeadState* state, 
 
 // ---- host ---------------------------------------------------------------------------------------
 
-// From this many multiplications N d V on, dH alone takes one pass: the product it saves is worth more
-// than the launches behind it that leave at once.
-constexpr double kOnePassWork = 1.0e10;
+// From this many multiplications (rows in whole tiles) x d x V on, dH alone takes one pass: the product
+// it saves is worth more than the launches behind it that leave at once, 2 us each (8.4e9: 79
+// against 84 us, 3.4e10 with 64 rows: 141 against 182; 2e9: 60 against 60).
+constexpr double kOnePassWork = 4.0e9;
 
 struct HeadPlan {
   int planes, plane;       // bf16 planes of an operand; elements of a plane's row
@@ -895,7 +905,7 @@ struct HeadPlan {
     copy_W = planes == 3 || plane != s.d;
     n_pad = (s.N + kTile - 1) / kTile * kTile;
     slots = (s.V + kTile - 1) / kTile;
-    one_pass = s.dH && !s.dW && static_cast<double>(s.N) * s.d * s.V >= kOnePassWork;
+    one_pass = s.dH && !s.dW && static_cast<double>(n_pad) * s.d * s.V >= kOnePassWork;
     const int64_t vmax = (static_cast<int64_t>(s.V) + kTile - 1) / kTile * kTile;
     int64_t cols = static_cast<int64_t>(kPieceBytes / (std::max<int64_t>(n_pad, 1) * 2 * planes)) / kTile * kTile;
     cols = std::min(std::max<int64_t>(cols, 4096), vmax);
@@ -903,11 +913,12 @@ struct HeadPlan {
     piece = static_cast<int>(((vmax + pieces - 1) / pieces + kTile - 1) / kTile * kTile);
     pieces = static_cast<int>((vmax + piece - 1) / piece);
     // few tiles of dH: its long sum over the vocabulary is split over the CTA pairs, at least
-    // kSplitBlocks blocks of 64 each
+    // kSplitBlocks blocks of 64 (of every kept product) each
     const int64_t out_tiles = n_pad / kTile * ((s.d + kTile - 1) / kTile);
     splits = 1;
-    if (s.dH && pieces == 1 && out_tiles > 0 && out_tiles < 74)
-      splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(74 / out_tiles, piece / kBK / kSplitBlocks)));
+    if (s.dH && out_tiles > 0 && out_tiles < 74)
+      splits = static_cast<int>(std::max<int64_t>(
+          1, std::min<int64_t>(74 / out_tiles, piece / kBK * (planes == 3 ? 6 : 1) / kSplitBlocks)));
     acc = s.dH && (pieces > 1 || splits > 1);
     ldacc = (s.d + 3) / 4 * 4;
     size_t o = 256;
@@ -933,28 +944,13 @@ struct HeadPlan {
   }
 };
 
-template <class Kern, class... Args>
-cudaError_t launch(bool pdl, Kern kernel, dim3 grid, unsigned block, size_t smem, cudaStream_t st, Args... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute a[1];
-  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  a[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = a;
-  cfg.numAttrs = pdl ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 template <int EPI, int PLANES>
 cudaError_t run_gemm(const HeadGemm& p, int64_t max_tiles, cudaStream_t st) {
   const void* k = reinterpret_cast<const void*>(head_gemm_kernel<EPI, PLANES>);
-  cudaError_t e = tc_configure_kernel(k, kSmem, kThreads);
+  cudaError_t e = lm_configure_kernel(k, kSmem);
   if (e != cudaSuccess) return e;
-  const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(tc_sm_count() / 2, max_tiles));
-  return launch(true, head_gemm_kernel<EPI, PLANES>, dim3(static_cast<unsigned>(2 * pairs)), kThreads, kSmem, st, p);
+  const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(lm_sm_count() / 2, max_tiles));
+  return lm_launch(true, head_gemm_kernel<EPI, PLANES>, dim3(static_cast<unsigned>(2 * pairs)), kThreads, kSmem, st, p);
 }
 
 template <class T, int PLANES>
@@ -978,14 +974,14 @@ cudaError_t run_head(const HeadShape& s, const T* H, const T* W, const void* lab
   float2* coef = pl.one_pass ? reinterpret_cast<float2*>(ws + pl.o_coef) : nullptr;
   const int direct = PLANES == 1 && !pl.copy_W;   // H itself can be an operand when every row is live
 
-  cudaError_t e = launch(false, head_rows_kernel, dim3(1), 1024, 0, st, labels, id_bytes, weights,
+  cudaError_t e = lm_launch(false, head_rows_kernel, dim3(1), 1024, 0, st, labels, id_bytes, weights,
                          static_cast<int>(s.N), s.V, state, rows, lab, wgt, loss);
   if (e == cudaSuccess && s.N > 0)
-    e = launch(true, head_gather_kernel<T, PLANES>, dim3(static_cast<unsigned>(pl.n_pad)), 128, 0, st, H, s.d, s.N,
+    e = lm_launch(true, head_gather_kernel<T, PLANES>, dim3(static_cast<unsigned>(pl.n_pad)), 128, 0, st, H, s.d, s.N,
                static_cast<const HeadState*>(state), static_cast<const int*>(rows), Hc, pl.plane, dH, direct, W,
                static_cast<const int*>(lab), pl.one_pass ? lse : nullptr);
   if (e == cudaSuccess && pl.copy_W)
-    e = launch(true, head_weights_kernel<T, PLANES>, dim3(s.V), 128, 0, st, W, s.d, Wc, pl.plane);
+    e = lm_launch(true, head_weights_kernel<T, PLANES>, dim3(s.V), 128, 0, st, W, s.d, Wc, pl.plane);
   if (e != cudaSuccess) return e;
   if (s.N == 0) return dW ? cudaMemsetAsync(dW, 0, static_cast<size_t>(s.V) * s.d * sizeof(T), st) : cudaSuccess;
 
@@ -994,11 +990,11 @@ cudaError_t run_head(const HeadShape& s, const T* H, const T* W, const void* lab
   CUtensorMap H_k, H_mn, W_k, W_mn, g_k, g_mn, X_k, X_mn;
   std::memset(&X_k, 0, sizeof(X_k));
   std::memset(&X_mn, 0, sizeof(X_mn));
-  bool ok = tc_map_2d(&H_k, Hc, pl.n_pad, wide, wide, kBK, kHalf) && tc_map_2d(&W_k, Wc, s.V, wide, wide, kBK, kHalf);
-  if (ok && direct) ok = tc_map_2d(&X_k, H, s.N, wide, wide, kBK, kHalf) && tc_map_2d(&X_mn, H, s.N, wide, wide, 64, kBK);
+  bool ok = lm_map_2d(&H_k, Hc, pl.n_pad, wide, wide, kBK, kHalf) && lm_map_2d(&W_k, Wc, s.V, wide, wide, kBK, kHalf);
+  if (ok && direct) ok = lm_map_2d(&X_k, H, s.N, wide, wide, kBK, kHalf) && lm_map_2d(&X_mn, H, s.N, wide, wide, 64, kBK);
   if (ok && grads)
-    ok = tc_map_2d(&H_mn, Hc, pl.n_pad, wide, wide, 64, kBK) && tc_map_2d(&W_mn, Wc, s.V, wide, wide, 64, kBK) &&
-         tc_map_2d(&g_k, g, pl.n_pad, gw, gw, kBK, kHalf) && tc_map_2d(&g_mn, g, pl.n_pad, gw, gw, 64, kBK);
+    ok = lm_map_2d(&H_mn, Hc, pl.n_pad, wide, wide, 64, kBK) && lm_map_2d(&W_mn, Wc, s.V, wide, wide, 64, kBK) &&
+         lm_map_2d(&g_k, g, pl.n_pad, gw, gw, kBK, kHalf) && lm_map_2d(&g_mn, g, pl.n_pad, gw, gw, 64, kBK);
   if (!ok) return cudaErrorInvalidValue;
 
   HeadGemm base;
@@ -1038,7 +1034,7 @@ cudaError_t run_head(const HeadShape& s, const T* H, const T* W, const void* lab
   auto losses = [&](bool exps, int only_retry) {
     const dim3 grid(static_cast<unsigned>((s.N + 31) / 32));
     auto go = [&](auto kernel) {
-      return launch(true, kernel, grid, 256, 0, st, static_cast<const HeadState*>(state), only_retry,
+      return lm_launch(true, kernel, grid, 256, 0, st, static_cast<const HeadState*>(state), only_retry,
                     static_cast<const float2*>(parts), pl.slots, pl.n_pad, static_cast<const float*>(target),
                     static_cast<const float*>(wgt), static_cast<const int*>(rows), lse, coef, loss);
     };
@@ -1064,7 +1060,7 @@ cudaError_t run_head(const HeadShape& s, const T* H, const T* W, const void* lab
     p.out = dH;
     cudaError_t e2 = run_gemm<DH, PLANES>(p, mt * dt * pl.splits, st);
     if (e2 == cudaSuccess && i + 1 == pl.pieces && pl.splits > 1)
-      e2 = launch(true, head_join_kernel<T>,
+      e2 = lm_launch(true, head_join_kernel<T>,
                   dim3((s.d + 255) / 256, static_cast<unsigned>(std::min<int64_t>(s.N, 4096))), 256, 0, st,
                   static_cast<const HeadState*>(state), only_retry, reinterpret_cast<const float*>(ws + pl.o_acc),
                   pl.splits, pl.n_pad, pl.ldacc, s.d, static_cast<const int*>(rows), p.coef,

@@ -168,10 +168,17 @@ __global__ void __launch_bounds__(kThreads) clip_kernel(StepShape sh, const floa
   for (int k = threadIdx.x; k < sh.part_stride; k += kThreads) ss += p[k];
   const float tot = block_sum(ss);
   if (threadIdx.x == 0) {
-    const float n = sqrtf(sh.extra_sq ? tot + sh.extra_sq[i] : tot);
+    const float n = sqrtf(tot);
     norms[i] = n;
     clip[i] = (n > sh.C) ? sh.C / n : 1.0f;
   }
+}
+
+// ---- squared norms of parameters beside the stack: added to each sample's first slot, so that
+// the clip's sum over the slots holds them ------------------------------------------------
+__global__ void __launch_bounds__(kThreads) add_extra_kernel(StepShape sh, const float* extra, float* partials) {
+  const int i = blockIdx.x * kThreads + threadIdx.x;
+  if (i < sh.B) partials[static_cast<size_t>(i) * sh.part_stride] += extra[i];
 }
 
 // ---- per-sample squared norms alone (the Hutchinson estimate): the sum of a sample's
@@ -451,6 +458,11 @@ cudaError_t simt_project_norm(const StepShape& sh, const LayerWs* ws, const Laye
 cudaError_t finalize_clip(const StepShape& sh, const float* partials, float* norms, float* clip,
                           cudaStream_t st) {
   clip_kernel<<<sh.B, kThreads, 0, st>>>(sh, partials, norms, clip);
+  return cudaGetLastError();
+}
+
+cudaError_t add_extra_sqnorms(const StepShape& sh, const float* extra, float* partials, cudaStream_t st) {
+  add_extra_kernel<<<cdiv(sh.B, kThreads), kThreads, 0, st>>>(sh, extra, partials);
   return cudaGetLastError();
 }
 

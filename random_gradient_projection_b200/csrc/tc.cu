@@ -1982,8 +1982,8 @@ struct ApTable {
 };
 
 __global__ void __launch_bounds__(256) clip_scale_kernel(ApTable t, int r, int T, int part_stride, float C,
-                                                         const float* partials, const float* extra_sq,
-                                                         float* norms, float* clip, int rescale) {
+                                                         const float* partials, float* norms, float* clip,
+                                                         int rescale) {
   __shared__ float red[8];
   __shared__ float c_sh;
   ptx::griddep_launch_dependents();
@@ -1999,7 +1999,7 @@ __global__ void __launch_bounds__(256) clip_scale_kernel(ApTable t, int r, int T
   if (threadIdx.x == 0) {
     float tot = 0.0f;
     for (int w = 0; w < 8; ++w) tot += red[w];
-    const float n = sqrtf(extra_sq ? tot + extra_sq[i] : tot);
+    const float n = sqrtf(tot);
     const float c = (n > C) ? C / n : 1.0f;
     if (l == 0) {
       norms[i] = n;
@@ -2204,23 +2204,17 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 }
 
 // bf16 row-major [rows][cols] as a 2-D map with a (box_cols x box_rows) box, 128-byte swizzle.
-// `ld`: elements from one row to the next.
-bool map_2d_ld(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t box_cols,
-               uint32_t box_rows) {
+bool map_2d(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint32_t box_cols,
+            uint32_t box_rows) {
   auto enc = encode_fn();
   if (!enc) return false;
   cuuint64_t dims[2] = {cols, rows};
-  cuuint64_t strides[1] = {ld * 2};
+  cuuint64_t strides[1] = {cols * 2};
   cuuint32_t box[2] = {box_cols, box_rows};
   cuuint32_t es[2] = {1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, es,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-bool map_2d(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint32_t box_cols,
-            uint32_t box_rows) {
-  return map_2d_ld(m, ptr, rows, cols, cols, box_cols, box_rows);
 }
 
 // fp32 row-major [rows][cols] as a 2-D map with a (32 x box_rows) box, 128-byte swizzle.
@@ -2898,7 +2892,7 @@ cudaError_t tc_clip_scale(const StepShape& sh, const LayerWs* ws, const TcWorksp
   for (int l = 0; l < sh.L; ++l) t.AP[l] = static_cast<__nv_bfloat16*>(ws[l].AP);
   ++*launches;
   return launch_pdl(clip_scale_kernel, dim3(sh.B, rescale_ap ? sh.L : 1), dim3(256), 0, st, t, sh.r, sh.T,
-                    sh.part_stride, sh.C, partials, sh.extra_sq, norms, clip, rescale_ap ? 1 : 0);
+                    sh.part_stride, sh.C, partials, norms, clip, rescale_ap ? 1 : 0);
 }
 
 cudaError_t tc_aggregate_stored(const StepShape& sh, const LayerWs* ws, const float* clip, cudaStream_t st,
@@ -3263,18 +3257,6 @@ __global__ void sum_slots_static_kernel(const float* partials, int slots, int B,
 size_t tc_static_scratch_bytes() { return kStaticScratchBytes; }
 
 bool tc_tensor_maps_available() { return encode_fn() != nullptr; }
-
-bool tc_map_2d(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t box_cols,
-               uint32_t box_rows) {
-  return map_2d_ld(m, ptr, rows, cols, ld, box_cols, box_rows);
-}
-
-int tc_sm_count() { return sm_count(); }
-
-cudaError_t tc_configure_kernel(const void* kernel, int smem, int threads) {
-  int per_sm = 0;
-  return configure_kernel(kernel, smem, threads, &per_sm);
-}
 
 size_t tc_static_scratch_needed(int d_in, int d_out, int r, int B, int T) {
   const size_t slots = static_cast<size_t>(tc_partials_per_sample(r, d_out));

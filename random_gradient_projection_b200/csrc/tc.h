@@ -1,6 +1,5 @@
 // Tensor-core (tcgen05 / TMEM / TMA) path of the DP-GRAPE step for bf16 inputs.
 #pragma once
-#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <string>
@@ -83,14 +82,6 @@ cudaError_t tc_backproject(const StepShape& sh, const LayerWs* ws, const LayerIo
 size_t tc_static_scratch_bytes();
 // Whether the driver provides the tensor-map encoder every tensor-core kernel needs.
 bool tc_tensor_maps_available();
-// bf16 row-major [rows][cols] with a row pitch of `ld` elements as a 2-D map of
-// (box_cols x box_rows) boxes, 128-byte swizzle.
-bool tc_map_2d(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t box_cols,
-               uint32_t box_rows);
-// SM count of the current device, and the opt-in to `smem` bytes of dynamic shared memory
-// for `kernel` on it (both taken once per device).
-int tc_sm_count();
-cudaError_t tc_configure_kernel(const void* kernel, int smem, int threads);
 size_t tc_static_scratch_needed(int d_in, int d_out, int r, int B, int T);
 cudaError_t tc_layer_sqnorms_static(const void* A, const void* G, int d_in, int d_out, int r, int B,
                                     int T, uint64_t seed, uint32_t layer, uint32_t step, float* out,

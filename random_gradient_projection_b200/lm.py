@@ -109,6 +109,10 @@ def _torch_dtype(dtype):
     raise ValueError(f"dtype: need 'bf16' or 'f32', got {dtype!r}")
 
 
+# the current stream's handle, without the stream object around it where torch offers that
+_raw_stream = getattr(getattr(torch, "_C", None), "_cuda_getCurrentRawStream", None)
+
+
 class _On:
     """Makes `stream` (None: the current one) current, so that what is allocated belongs to it;
     entering gives its handle."""
@@ -118,6 +122,8 @@ class _On:
 
     def __enter__(self):
         if self.stream is None:
+            if _raw_stream is not None:
+                return _raw_stream(torch.cuda.current_device())
             return torch.cuda.current_stream().cuda_stream
         handle = self.stream if isinstance(self.stream, int) else self.stream.cuda_stream
         self.inner = torch.cuda.stream(torch.cuda.ExternalStream(handle))
