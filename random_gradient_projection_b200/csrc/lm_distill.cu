@@ -137,6 +137,15 @@ __device__ __forceinline__ void exps_low(const uint4& raw, float ref, float scal
   for (int i = 0; i < Unit<T>::kN / 2; ++i)
     e[i] = pair(ex2((v[2 * i] - ref) * scale), ex2((v[2 * i + 1] - ref) * scale));
 }
+template <class T>
+__device__ __forceinline__ float sum_of(uint64_t (&e)[Unit<T>::kN / 2]) {
+#pragma unroll
+  for (int o = 1; o < Unit<T>::kN / 2; o <<= 1)
+#pragma unroll
+    for (int i = 0; i + o < Unit<T>::kN / 2; i += 2 * o) e[i] = add2(e[i], e[i + o]);
+  const float2 x = unpair(e[0]);
+  return x.x + x.y;
+}
 // f times the pairs, as a unit.
 template <class T>
 __device__ __forceinline__ uint4 scaled(const uint64_t (&e)[Unit<T>::kN / 2], float f) {
@@ -345,8 +354,8 @@ __global__ void __launch_bounds__(THREADS, MINB) distill_kernel(const DistillPar
 }
 
 // ---- long rows: streamed through shared memory ------------------------------------------------
-// A CTA takes rows in turn and moves them through a ring of 16 KB slots in shared memory, one bulk
-// copy per slot each way.  Sixteen warps do the arithmetic in place, in two passes over the row's
+// A CTA takes rows in turn and moves them through a ring of slots of 16 or 24 KB in shared memory, one
+// bulk copy per slot each way.  Sixteen or twenty-four warps do the arithmetic in place, in two passes over the row's
 // chunks: maximum and sum as they arrive, then the gradient, chunk by chunk, after which a chunk is
 // stored and its slot loaded with the next row's data.  So memory does not wait for the
 // exponentials (two per element: for bf16 their unit alone takes 0.8 of the row's time on the bus)
@@ -358,16 +367,17 @@ __global__ void __launch_bounds__(THREADS, MINB) distill_kernel(const DistillPar
 // Chunks of a row in the order of their slots: its n chunks, then (n > kSlots) the first
 // over = n - kSlots of them again.  Slots come free in the same order: an `over` chunk after the
 // first pass, every other one when its gradient has been stored.
-constexpr int kRowThreads = 512, kTeachThreads = 128, kCopyWarps = 2;
-constexpr int kRowBlock = kRowThreads + kTeachThreads + 32 * kCopyWarps;
+constexpr int kTeachThreads = 128, kCopyWarps = 2;
 constexpr int kRowTeacher = kTeachThreads;   // entries of a row at most: one per thread
-constexpr int kChunk = 2 * kRowThreads;      // 16-byte units: two per thread
-constexpr int kChunkBytes = kChunk * 16;
 constexpr int kStatRing = 16;
 constexpr uint64_t kWaitNs = 4000000000ull;
+// MINB CTAs on an SM: threads that do the arithmetic, 16-byte units of a chunk (two per thread), slots.
 template <int MINB>
-struct RowRing {
-  static constexpr int kSlots = MINB == 1 ? 13 : 6;   // of 16 KB, with one or two CTAs on an SM
+struct RowCfg {
+  static constexpr int kThreads = MINB == 1 ? 768 : 512;
+  static constexpr int kBlock = kThreads + kTeachThreads + 32 * kCopyWarps;
+  static constexpr int kChunk = 2 * kThreads, kChunkBytes = kChunk * 16;
+  static constexpr int kSlots = (MINB == 1 ? 216 : 96) * 1024 / kChunkBytes;
   static_assert(kTeachThreads == 128 && kSlots < kStatRing, "a row's statistics outlive its slots");
 };
 
@@ -376,7 +386,7 @@ __device__ __forceinline__ void bar_sync() { asm volatile("bar.sync %0, %1;" ::"
 constexpr int kBarRow = 1, kBarTeach = 2;
 
 // The 16-byte units of a row, its elements outside them, and its chunks.
-template <class T, int SLOTS>
+template <class T, class CFG>
 struct RowGeo {
   int head, rest0, units;   // elements before the units, first element after them; units
   int n, over;              // chunks; those that are loaded twice
@@ -386,14 +396,14 @@ struct RowGeo {
     head = min(V, mis ? kN - mis : 0);
     units = (V - head) / kN;
     rest0 = head + units * kN;
-    n = (units + kChunk - 1) / kChunk;
-    over = max(0, n - SLOTS);
+    n = (units + CFG::kChunk - 1) / CFG::kChunk;
+    over = max(0, n - CFG::kSlots);
   }
   // chunk of the e-th slot of the row, and whether its gradient is stored from there
   __device__ __forceinline__ int chunk(int e) const { return e < n ? e : e - n; }
   __device__ __forceinline__ bool stored(int e) const { return e >= over; }
   __device__ __forceinline__ uint32_t bytes(int c) const {
-    return static_cast<uint32_t>(min(kChunk, units - c * kChunk)) * 16;
+    return static_cast<uint32_t>(min(CFG::kChunk, units - c * CFG::kChunk)) * 16;
   }
 };
 
@@ -409,10 +419,13 @@ __device__ __forceinline__ int64_t next_row(const DistillParams& p, int64_t row,
 }
 
 template <class T, int MINB>
-__global__ void __launch_bounds__(kRowBlock, MINB)
+__global__ void __launch_bounds__(RowCfg<MINB>::kBlock, MINB)
     distill_rows_kernel(const DistillParams p, const T* logits, T* Gout) {
-  constexpr int kN = Unit<T>::kN, kWarps = kRowThreads / 32, kSlots = RowRing<MINB>::kSlots;
-  using Geo = RowGeo<T, kSlots>;
+  using Cfg = RowCfg<MINB>;
+  constexpr int kRowThreads = Cfg::kThreads, kRowBlock = Cfg::kBlock, kChunk = Cfg::kChunk;
+  constexpr int kChunkBytes = Cfg::kChunkBytes, kSlots = Cfg::kSlots;
+  constexpr int kN = Unit<T>::kN, kWarps = kRowThreads / 32;
+  using Geo = RowGeo<T, Cfg>;
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ uint64_t full[kSlots], computed[kSlots], patched[kSlots], ready[2];
   __shared__ float2 red[2][kWarps], stats[kStatRing];
@@ -669,28 +682,38 @@ __global__ void __launch_bounds__(kRowBlock, MINB)
         wait(&full[sl], ph);
         const uint4* buf = reinterpret_cast<const uint4*>(ring + sl * kChunkBytes);
         const int left = g.units - c * kChunk;   // units of this chunk and the ones after it
-        const uint4 x0 = tid < left ? buf[tid] : unit_none(T());
-        const uint4 x1 = tid + kRowThreads < left ? buf[tid + kRowThreads] : unit_none(T());
-        const float m0 = m;
-        m = fmaxf(m, fmaxf(unit_max(x0, T()), unit_max(x1, T())));
-        const float ref = Running::ref(m);
-        s *= ex2((m0 - ref) * p.scale);
-        uint64_t e0[kN / 2], e1[kN / 2];
-        if (ref > kLowRef) {
-          exps<T>(x0, ref, p.scale, e0);
-          exps<T>(x1, ref, p.scale, e1);
-        } else {
-          exps_low<T>(x0, ref, p.scale, e0);
-          exps_low<T>(x1, ref, p.scale, e1);
+        if (left >= kChunk) {
+          const uint4 x0 = buf[tid], x1 = buf[tid + kRowThreads];
+          const float m0 = m;
+          m = fmaxf(m, fmaxf(unit_max(x0, T()), unit_max(x1, T())));
+          const float ref = Running::ref(m);
+          s *= ex2((m0 - ref) * p.scale);
+          uint64_t e0[kN / 2], e1[kN / 2];
+          if (ref > kLowRef) {
+            exps<T>(x0, ref, p.scale, e0);
+            exps<T>(x1, ref, p.scale, e1);
+          } else {
+            exps_low<T>(x0, ref, p.scale, e0);
+            exps_low<T>(x1, ref, p.scale, e1);
+          }
+#pragma unroll
+          for (int i = 0; i < kN / 2; ++i) e0[i] = add2(e0[i], e1[i]);
+          s += sum_of<T>(e0);
+        } else {   // the row's last chunk: warps past its end do nothing
+          for (int u = tid; (u & ~31) < left; u += kRowThreads) {
+            const uint4 x = u < left ? buf[u] : unit_none(T());
+            const float m0 = m;
+            m = fmaxf(m, unit_max(x, T()));
+            const float ref = Running::ref(m);
+            s *= ex2((m0 - ref) * p.scale);
+            uint64_t e[kN / 2];
+            if (ref > kLowRef)
+              exps<T>(x, ref, p.scale, e);
+            else
+              exps_low<T>(x, ref, p.scale, e);
+            s += sum_of<T>(e);
+          }
         }
-#pragma unroll
-        for (int i = 0; i < kN / 2; ++i) e0[i] = add2(e0[i], e1[i]);
-#pragma unroll
-        for (int o = 1; o < kN / 2; o <<= 1)
-#pragma unroll
-          for (int i = 0; i + o < kN / 2; i += 2 * o) e0[i] = add2(e0[i], e0[i + o]);
-        const float2 e = unpair(e0[0]);
-        s += e.x + e.y;
         if (c < g.over) release(sl);
         if (++sl == kSlots) sl = 0, ph ^= 1;
       }
@@ -769,11 +792,12 @@ cudaError_t run(const DistillParams& p, const void* logits, void* Gout, cudaStre
 
 template <class T, int MINB>
 cudaError_t run_rows(const DistillParams& p, const void* logits, void* Gout, cudaStream_t st) {
-  const int smem = RowRing<MINB>::kSlots * kChunkBytes;
+  using Cfg = RowCfg<MINB>;
+  const int smem = Cfg::kSlots * Cfg::kChunkBytes;
   cudaError_t e = lm_configure_kernel(reinterpret_cast<const void*>(distill_rows_kernel<T, MINB>), smem);
   if (e != cudaSuccess) return e;
   const int64_t grid = std::min<int64_t>(p.N, static_cast<int64_t>(MINB) * lm_sm_count());
-  distill_rows_kernel<T, MINB><<<static_cast<unsigned>(grid), kRowBlock, smem, st>>>(
+  distill_rows_kernel<T, MINB><<<static_cast<unsigned>(grid), Cfg::kBlock, smem, st>>>(
       p, static_cast<const T*>(logits), static_cast<T*>(Gout));
   return cudaGetLastError();
 }
@@ -782,7 +806,8 @@ cudaError_t run_rows(const DistillParams& p, const void* logits, void* Gout, cud
 //  - up to 32 KB, 128 threads a row and eight rows an SM, the part of a row beyond their registers
 //    coming from L2 a second time (bf16 V = 8192: 77 against 103 for the ring; V = 4000: 51 against 96);
 //  - beyond, the ring, with two CTAs on an SM up to 64 KB (bf16 V = 32000: 229 against 249 with one)
-//    and one from there on (bf16 V = 128000: 817 against 891; fp32 V = 32000: 341 against 368);
+//    and one from there on, with half as many threads again (bf16 V = 128000: 773, with 512 threads 820,
+//    and 891 with two; fp32 V = 32000: 349 against 368);
 //  - long rows with more than 128 teacher entries: 512 threads and two rows an SM, otherwise as
 //    the first (bf16 V = 128000: 1041).
 constexpr int64_t kShortUpTo = 32768, kTwoUpTo = 65536;
