@@ -355,14 +355,17 @@ __global__ void __launch_bounds__(THREADS, MINB) distill_kernel(const DistillPar
 
 // ---- long rows: streamed through shared memory ------------------------------------------------
 // A CTA takes rows in turn and moves them through a ring of slots of 16 or 24 KB in shared memory, one
-// bulk copy per slot each way.  Sixteen or twenty-four warps do the arithmetic in place, in two passes over the row's
-// chunks: maximum and sum as they arrive, then the gradient, chunk by chunk, after which a chunk is
-// stored and its slot loaded with the next row's data.  So memory does not wait for the
+// bulk copy per slot each way.  Sixteen or twenty-four warps do the arithmetic in place, in two
+// passes over the row's chunks: maximum and sum as they arrive, then the gradient, chunk by chunk,
+// after which a chunk is stored and its slot loaded with the next row's data.  So memory does not wait for the
 // exponentials (two per element: for bf16 their unit alone takes 0.8 of the row's time on the bus)
-// nor for the reductions.  A row longer than the ring has its first chunks loaded twice, the
+// nor for the reductions.  Bound by instruction issue, next to memory: 4096 x 50265 bf16 takes 174 us
+// (4.7 TB/s), 8192 x 128000 799 (5.3 TB/s), 4096 x 50265 fp32 290 (5.7 TB/s).  A row longer than the ring has its first chunks loaded twice, the
 // second time from L2; otherwise DRAM and L2 see every logit once and every gradient once.
 // Four warps work on the teacher's entries: they prepare the next row's while a row is summed, and put
-// their mass into each finished chunk before it is stored.  One thread issues all copies.
+// their mass into each finished chunk before it is stored.  Two threads issue the copies, each those
+// of every other slot: waiting until a slot has been read out takes a microsecond, which one thread
+// alone could not hide.
 //
 // Chunks of a row in the order of their slots: its n chunks, then (n > kSlots) the first
 // over = n - kSlots of them again.  Slots come free in the same order: an `over` chunk after the

@@ -49,7 +49,9 @@
 // A's rows and half of B's columns in its ring of shared-memory stages.  Warp 17 of each
 // CTA loads by TMA, warp 16 of CTA 0 issues the MMAs for both, warps 0-15 are the epilogue of their
 // CTA's 128 rows (each 32 rows x 64 columns, in registers); two 256-column accumulators in TMEM
-// let it overlap the next sums.
+// let it overlap the next sums.  Bound by the tensor pipe where d is large: at 8192 x 4096 x 32000 EXP
+// runs at 1547 and DH at 1564 TFLOP/s in bursts (a library product of that size: 1596), both at 1262
+// under the power cap (library 1376); with d of a few hundred the epilogue's exponentials bound it.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -710,21 +712,91 @@ __global__ void __launch_bounds__(1024) head_rows_kernel(const void* labels, int
 // Row r of the compact H (bf16, or three planes of fp32), a CTA per row: the live rows, then zero
 // rows up to a whole tile; nothing where the products can read H itself (`direct` and every row
 // live).  Dropped rows of dH are zeroed.  ref (not null): the label's logit of each live row.
-template <class T, int PLANES>
-__global__ void __launch_bounds__(128) head_gather_kernel(const T* H, int d, int64_t N, const HeadState* state,
-                                                          const int* rows, __nv_bfloat16* Hc, int plane, T* dH,
-                                                          int direct, const T* W, const int* labels, float* ref) {
+// With few rows (FEW: at most kFewRows) there is no launch of head_rows_kernel before: every CTA counts
+// the live rows itself, and writes its own row's entry of what that kernel writes.
+constexpr int kFewRows = 1024, kFewPer = kFewRows / 128;
+struct FewRows {
+  const void* labels;
+  int id_bytes, V;
+  const float* weights;
+  float* wgt;
+  float* loss;
+};
+template <class T, int PLANES, bool FEW>
+__global__ void __launch_bounds__(128) head_gather_kernel(const T* H, int d, int64_t N, HeadState* state, int* rows,
+                                                          __nv_bfloat16* Hc, int plane, T* dH, int direct, const T* W,
+                                                          int* labels, float* ref, const FewRows few) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   __shared__ float red[4];
   const int64_t r = blockIdx.x;
-  const int n_live = __ldcg(&state->n_live);
+  int n_live, row = -1, label = 0;
+  if (FEW) {
+    __shared__ int count[4], found[2];
+    const int tid = threadIdx.x, n0 = tid * kFewPer;   // a thread's rows are consecutive
+    int lab[kFewPer];
+    float w[kFewPer];
+    int mine = 0;
+#pragma unroll
+    for (int k = 0; k < kFewPer; ++k) {
+      lab[k] = n0 + k < N ? label_at(few.labels, few.id_bytes, n0 + k, few.V) : -1;
+      w[k] = n0 + k < N && few.weights ? few.weights[n0 + k] : 1.0f;
+    }
+#pragma unroll
+    for (int k = 0; k < kFewPer; ++k) {
+      if (w[k] == 0.0f) lab[k] = -1;
+      mine += lab[k] >= 0;
+    }
+    int before = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, before, o);
+      if ((tid & 31) >= o) before += y;
+    }
+    if ((tid & 31) == 31) count[tid >> 5] = before;
+    __syncthreads();
+    before -= mine;
+    for (int k = 0; k < tid >> 5; ++k) before += count[k];
+    n_live = count[0] + count[1] + count[2] + count[3];
+    // the r-th live row, or from the end backwards the dropped ones
+#pragma unroll
+    for (int k = 0; k < kFewPer; ++k) {
+      const int n = n0 + k;
+      const int at = lab[k] >= 0 ? before : static_cast<int>(N) - 1 - (n - before);
+      if (n < N && at == r) {
+        found[0] = n;
+        found[1] = lab[k];
+        rows[r] = n;
+        if (lab[k] >= 0) {
+          labels[r] = lab[k];
+          few.wgt[r] = w[k];
+        } else {
+          few.loss[n] = 0.0f;
+        }
+      }
+      before += lab[k] >= 0;
+    }
+    if (r == 0 && tid == 0) {
+      state->err = 0;
+      state->n_live = n_live;
+      state->retry = 0;
+    }
+    __syncthreads();
+    if (r < N) {
+      row = found[0];
+      label = found[1];
+    }
+  } else {
+    n_live = __ldcg(&state->n_live);
+    if (r < N) row = __ldcg(rows + r);
+    if (ref && r < n_live) label = __ldcg(labels + r);
+  }
   const int64_t fill = (static_cast<int64_t>(n_live) + kTile - 1) / kTile * kTile;
   const bool copy = !(direct && n_live == N);
   __nv_bfloat16* dst = Hc + r * plane * PLANES;
   if (r < n_live) {
-    const T* src = H + static_cast<int64_t>(__ldcg(rows + r)) * d;
-    const T* wl = ref ? W + static_cast<int64_t>(__ldcg(labels + r)) * d : nullptr;
+    const T* src = H + static_cast<int64_t>(row) * d;
+    const T* wl = ref ? W + static_cast<int64_t>(label) * d : nullptr;
     float dot = 0.0f;
     if (PLANES == 1 && d % 8 == 0) {
       for (int c = threadIdx.x; c < d / 8; c += 128) {
@@ -764,7 +836,7 @@ __global__ void __launch_bounds__(128) head_gather_kernel(const T* H, int d, int
   if (copy && r < fill)
     for (int c = threadIdx.x; c < plane * PLANES / 8; c += 128) reinterpret_cast<uint4*>(dst)[c] = make_uint4(0, 0, 0, 0);
   if (r < N && dH) {
-    T* o = dH + static_cast<int64_t>(__ldcg(rows + r)) * d;
+    T* o = dH + static_cast<int64_t>(row) * d;
     for (int c = threadIdx.x; c < d; c += 128) o[c] = static_cast<T>(0.0f);
   }
 }
@@ -974,16 +1046,23 @@ cudaError_t run_head(const HeadShape& s, const T* H, const T* W, const void* lab
   float2* coef = pl.one_pass ? reinterpret_cast<float2*>(ws + pl.o_coef) : nullptr;
   const int direct = PLANES == 1 && !pl.copy_W;   // H itself can be an operand when every row is live
 
-  cudaError_t e = lm_launch(false, head_rows_kernel, dim3(1), 1024, 0, st, labels, id_bytes, weights,
-                         static_cast<int>(s.N), s.V, state, rows, lab, wgt, loss);
-  if (e == cudaSuccess && s.N > 0)
-    e = lm_launch(true, head_gather_kernel<T, PLANES>, dim3(static_cast<unsigned>(pl.n_pad)), 128, 0, st, H, s.d, s.N,
-               static_cast<const HeadState*>(state), static_cast<const int*>(rows), Hc, pl.plane, dH, direct, W,
-               static_cast<const int*>(lab), pl.one_pass ? lse : nullptr);
+  if (s.N == 0) return dW ? cudaMemsetAsync(dW, 0, static_cast<size_t>(s.V) * s.d * sizeof(T), st) : cudaSuccess;
+  cudaError_t e = cudaSuccess;
+  const bool few = s.N <= kFewRows;
+  if (!few)
+    e = lm_launch(false, head_rows_kernel, dim3(1), 1024, 0, st, labels, id_bytes, weights, static_cast<int>(s.N), s.V,
+                  state, rows, lab, wgt, loss);
+  if (e == cudaSuccess) {
+    auto gather = [&](auto kernel) {
+      return lm_launch(!few, kernel, dim3(static_cast<unsigned>(pl.n_pad)), 128, 0, st, H, s.d, s.N, state, rows, Hc,
+                       pl.plane, dH, direct, W, lab, pl.one_pass ? lse : nullptr,
+                       FewRows{labels, id_bytes, s.V, weights, wgt, loss});
+    };
+    e = few ? gather(head_gather_kernel<T, PLANES, true>) : gather(head_gather_kernel<T, PLANES, false>);
+  }
   if (e == cudaSuccess && pl.copy_W)
     e = lm_launch(true, head_weights_kernel<T, PLANES>, dim3(s.V), 128, 0, st, W, s.d, Wc, pl.plane);
   if (e != cudaSuccess) return e;
-  if (s.N == 0) return dW ? cudaMemsetAsync(dW, 0, static_cast<size_t>(s.V) * s.d * sizeof(T), st) : cudaSuccess;
 
   // operand views: K-major boxes of 64 x 128 rows, M/N-major boxes of 64 x 64
   const bool grads = s.dH || s.dW;
