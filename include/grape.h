@@ -421,7 +421,7 @@ GRAPE_API int grape_layer_sqnorms_static(const void* A, const void* Gout, int32_
  * reused as soon as the call's work is done, and two calls whose work may overlap need one
  * each.  Device pointers of matrices, workspaces and outputs are 16-byte aligned; ids,
  * weights and per-row vectors need the alignment of their elements.  Token numbers (ids, labels, teacher
- * indices) are int32 or int64: id_bytes is 4 or 8.  A number outside [0, vocab) is no error:
+ * indices) are int32 or int64: id_bytes is 4 or 8.  vocab lies in [1, 2^30], d in [1, 2^20].  A number outside [0, vocab) is no error:
  * it means "no token" as each call states.  Errors are reported through
  * grape_global_error(): GRAPE_EINVAL (arguments), GRAPE_EUNSUPPORTED (not an sm_100a device,
  * or no tensor-map encoder in the driver), GRAPE_ECUDA. */

@@ -70,11 +70,14 @@ int guarded(const char* name, F&& f) {
 }
 
 constexpr int64_t kMaxIds = int64_t(1) << 30;
+constexpr int32_t kMaxVocab = 1 << 30, kMaxWidth = 1 << 20;
+const char* const kVocabRange = "vocab must lie in [1, 2^30]";
+const char* const kWidthRange = "d must lie in [1, 2^20]";
 
 const char* ids_problem(const void* ids, int32_t id_bytes, int64_t n, int32_t vocab) {
   if (id_bytes != 4 && id_bytes != 8) return "id_bytes must be 4 or 8";
   if (n < 0 || n > kMaxIds) return "the number of ids must lie in [0, 2^30]";
-  if (vocab < 1) return "vocab must be >= 1";
+  if (vocab < 1 || vocab > kMaxVocab) return kVocabRange;
   if (n > 0 && !ids) return "ids must not be null";
   if (!aligned(ids, static_cast<size_t>(id_bytes))) return "ids must be aligned to their element size";
   return nullptr;
@@ -82,15 +85,15 @@ const char* ids_problem(const void* ids, int32_t id_bytes, int64_t n, int32_t vo
 
 const char* batch_problem(int32_t B, int32_t T, int32_t vocab, int32_t d) {
   if (B < 0 || T < 0 || static_cast<int64_t>(B) * T > kMaxIds) return "need B, T >= 0 and B*T <= 2^30";
-  if (vocab < 1 || d < 1) return "vocab and d must be >= 1";
+  if (vocab < 1 || vocab > kMaxVocab) return kVocabRange;
+  if (d < 1 || d > kMaxWidth) return kWidthRange;
   return nullptr;
 }
 
 const char* head_problem(int64_t N, int32_t d, int32_t vocab, int32_t dtype) {
   if (N < 0 || N > kMaxIds) return "N must lie in [0, 2^30]";
-  if (d < 1 || vocab < 1) return "d and vocab must be >= 1";
-  if (d > (1 << 20)) return "d must be <= 2^20";
-  if (vocab > (1 << 30)) return "vocab must be <= 2^30";
+  if (vocab < 1 || vocab > kMaxVocab) return kVocabRange;
+  if (d < 1 || d > kMaxWidth) return kWidthRange;
   if (!dtype_ok(dtype)) return "dtype must be GRAPE_F32 or GRAPE_BF16";
   if ((N / 256 + 1) * (static_cast<int64_t>(vocab) / 256 + 1) > 0x7fffffff ||
       (N / 256 + 1) * (static_cast<int64_t>(d) / 256 + 1) > 0x7fffffff)
@@ -106,7 +109,7 @@ int grape_embed(const void* table, int32_t table_dtype, const void* ids, int32_t
                 int32_t vocab, int32_t d, double scale, int32_t out_dtype, void* out, void* stream) {
   return guarded("grape_embed", [&]() -> int {
     if (const char* m = ids_problem(ids, id_bytes, n_ids, vocab)) return einval(m);
-    if (d < 1) return einval("d must be >= 1");
+    if (d < 1 || d > kMaxWidth) return einval(kWidthRange);
     if (!dtype_ok(table_dtype) || !dtype_ok(out_dtype)) return einval("dtypes must be GRAPE_F32 or GRAPE_BF16");
     if (!std::isfinite(scale)) return einval("scale must be finite");
     if (n_ids == 0) return GRAPE_OK;
@@ -213,7 +216,7 @@ int grape_distill_loss(const void* logits, int32_t dtype, int64_t N, int32_t voc
     if (!dtype_ok(dtype) || !dtype_ok(value_dtype)) return einval("dtypes must be GRAPE_F32 or GRAPE_BF16");
     if (id_bytes != 4 && id_bytes != 8) return einval("id_bytes must be 4 or 8");
     if (N < 0 || N > 0x7fffffff) return einval("N must lie in [0, 2^31 - 1]");
-    if (vocab < 1) return einval("vocab must be >= 1");
+    if (vocab < 1 || vocab > kMaxVocab) return einval(kVocabRange);
     if (K < 1 || K > grape::kMaxTeacher) return einval("K must lie in [1, 1024]");
     if (!(temperature > 0) || !std::isfinite(temperature)) return einval("temperature must be positive and finite");
     if (N == 0) return GRAPE_OK;

@@ -210,7 +210,7 @@ def check_head(H, W, labels, w, **kw):
 
 
 HEAD = [(64, 64, 256), (1, 8, 1), (1, 64, 1000), (256, 256, 512), (300, 264, 1000), (257, 72, 2049), (130, 1024, 700),
-        (512, 512, 5003), (77, 100, 333), (33, 31, 257), (1000, 136, 12000)]
+        (512, 512, 5003), (77, 100, 333), (33, 31, 257), (1000, 136, 12000), (1024, 64, 600), (1025, 72, 600)]
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
@@ -241,6 +241,9 @@ def test_head_masked_rows_cost_nothing_and_reach_nothing(dt):
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_head_without_a_live_row(dt):
+    H, W, labels, _ = head_inputs(2000, 512, 9000, dt)     # of a size for one pass
+    got = lm.head_loss(H, W, torch.full_like(labels, -100))
+    assert not got.loss.any() and not got.dH.any()
     H, W, labels, _ = head_inputs(40, 64, 300, dt)
     got = lm.head_loss(H, W, torch.full_like(labels, -100), weight_grad=True)
     assert not got.loss.any() and not got.dH.any() and not got.dW.any()

@@ -35,7 +35,7 @@ EMBED = dict(table=P, tdt=F32, ids=P, id_bytes=8, n=4, V=10, d=8, scale=1.0, odt
 
 @pytest.mark.parametrize("kw,msg", [
     (dict(tdt=2), "dtypes"), (dict(odt=-1), "dtypes"), (dict(id_bytes=2), "id_bytes"), (dict(n=-1), "number of ids"),
-    (dict(n=(1 << 30) + 1), "number of ids"), (dict(V=0), "vocab"), (dict(d=0), "d must"), (dict(ids=0), "ids"),
+    (dict(n=(1 << 30) + 1), "number of ids"), (dict(V=0), "vocab"), (dict(V=(1 << 30) + 1), "vocab"), (dict(d=0), "d must"), (dict(d=(1 << 20) + 1), "d must"), (dict(ids=0), "ids"),
     (dict(ids=P + 4), "ids"), (dict(table=0), "null"), (dict(out=P + 8), "aligned"), (dict(scale=float("nan")), "scale")])
 def test_embed_refuses(lib, kw, msg):
     assert msg in refused(grape.grape_embed, *edit(EMBED, **kw))
@@ -46,7 +46,7 @@ def test_embed_of_nothing_is_a_no_op(lib):
 
 
 @pytest.mark.parametrize("kw,msg", [
-    (dict(B=-1), "B, T"), (dict(T=-1), "B, T"), (dict(B=1 << 20, T=1 << 20), "2^30"), (dict(V=0), "vocab"), (dict(d=0), "vocab and d"),
+    (dict(B=-1), "B, T"), (dict(T=-1), "B, T"), (dict(B=1 << 20, T=1 << 20), "2^30"), (dict(V=0), "vocab"), (dict(V=(1 << 30) + 1), "vocab"), (dict(d=0), "d must"), (dict(d=(1 << 20) + 1), "d must"),
     (dict(dtype=5), "dtype"), (dict(G=0), "Gout"), (dict(G=P + 2), "Gout"), (dict(ws=0), "workspace"),
     (dict(order=P + 4), "order"), (dict(out=0), "not be null"), (dict(scale=float("inf")), "scale")])
 def test_embed_sums_refuse(lib, kw, msg):
@@ -67,8 +67,8 @@ HEAD = dict(H=P, W=P, labels=P, id_bytes=8, w=0, N=4, d=8, V=10, dtype=BF16, ws=
 
 
 @pytest.mark.parametrize("kw,msg", [
-    (dict(N=-1), "N must"), (dict(N=(1 << 30) + 1), "N must"), (dict(d=0), "d and vocab"), (dict(V=0), "d and vocab"),
-    (dict(d=(1 << 20) + 1), "2^20"), (dict(N=1 << 30, V=1 << 29), "too large"), (dict(dtype=3), "dtype"),
+    (dict(N=-1), "N must"), (dict(N=(1 << 30) + 1), "N must"), (dict(d=0), "d must"), (dict(V=0), "vocab"),
+    (dict(d=(1 << 20) + 1), "d must"), (dict(V=(1 << 30) + 1), "vocab"), (dict(N=1 << 30, V=1 << 29), "too large"), (dict(dtype=3), "dtype"),
     (dict(id_bytes=1), "id_bytes"), (dict(labels=0), "ids"), (dict(labels=P + 2), "ids"), (dict(W=0), "W must"),
     (dict(W=P + 8), "W must"), (dict(H=0), "H and loss"), (dict(loss=0), "H and loss"), (dict(H=P + 2), "aligned"),
     (dict(dH=P + 4), "aligned"), (dict(dW=P + 4), "aligned"), (dict(ws=0), "workspace"), (dict(w=P + 2), "aligned")])
@@ -81,7 +81,7 @@ DISTILL = dict(z=P, dtype=F32, N=4, V=10, idx=P, id_bytes=4, val=P, vdt=F32, K=3
 
 @pytest.mark.parametrize("kw,msg", [
     (dict(dtype=2), "dtypes"), (dict(vdt=2), "dtypes"), (dict(id_bytes=3), "id_bytes"), (dict(N=-1), "N must"),
-    (dict(N=1 << 31), "N must"), (dict(V=0), "vocab"), (dict(K=0), "K must"), (dict(K=1025), "K must"), (dict(tau=0.0), "temperature"),
+    (dict(N=1 << 31), "N must"), (dict(V=0), "vocab"), (dict(V=(1 << 30) + 1), "vocab"), (dict(K=0), "K must"), (dict(K=1025), "K must"), (dict(tau=0.0), "temperature"),
     (dict(tau=-1.0), "temperature"), (dict(tau=float("inf")), "temperature"), (dict(z=0), "null"), (dict(out=0), "null"),
     (dict(z=P + 4), "16-byte"), (dict(idx=P + 2), "element size"), (dict(val=P + 2), "element size"), (dict(w=P + 1), "element size")])
 def test_distill_refuses(lib, kw, msg):
