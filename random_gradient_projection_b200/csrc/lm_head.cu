@@ -929,26 +929,42 @@ __global__ void __launch_bounds__(256) head_loss_kernel(const HeadState* state, 
   }
 }
 
-// dH from the splits of the vocabulary, added in order (and, after EXP, the coefficients applied).
+// dH from the splits of the vocabulary, added in order (and, after EXP, the coefficients applied).  A
+// thread takes four columns, eight splits' values in flight; at most kJoinBlocks CTAs, so that a
+// launch that leaves at once costs little (1000 rows of 1000: 8 us with a CTA a row).
+constexpr int kJoinThreads = 128, kJoinBlocks = 592;
 template <class T>
-__global__ void __launch_bounds__(256) head_join_kernel(const HeadState* state, int only_retry, const float* acc,
-                                                        int splits, int64_t n_pad, int64_t ldacc, int d,
-                                                        const int* rows, const float2* coef, const int* labels,
-                                                        const T* W, T* dH) {
+__global__ void __launch_bounds__(kJoinThreads) head_join_kernel(const HeadState* state, int only_retry,
+                                                                 const float* acc, int splits, int64_t n_pad,
+                                                                 int64_t ldacc, int d, const int* rows,
+                                                                 const float2* coef, const int* labels, const T* W,
+                                                                 T* dH) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   if (only_retry && __ldcg(&state->retry) == 0) return;
   const int n_live = __ldcg(&state->n_live);
+  const int c = 4 * (blockIdx.x * kJoinThreads + threadIdx.x);
+  if (c >= d) return;
   for (int64_t r = blockIdx.y; r < n_live; r += gridDim.y) {
-    const int c = blockIdx.x * 256 + threadIdx.x;
-    if (c >= d) continue;
-    float x = 0.0f;
-    for (int s = 0; s < splits; ++s) x += __ldcg(acc + (s * n_pad + r) * ldacc + c);
+    const int64_t row = __ldcg(rows + r);
+    float x[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int s0 = 0; s0 < splits; s0 += 8) {
+      float4 y[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        y[u] = s0 + u < splits ? __ldcg(reinterpret_cast<const float4*>(acc + ((s0 + u) * n_pad + r) * ldacc + c))
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) x[0] += y[u].x, x[1] += y[u].y, x[2] += y[u].z, x[3] += y[u].w;
+    }
     if (coef) {
       const float2 co = __ldcg(coef + r);
-      x = co.x * x - co.y * static_cast<float>(W[static_cast<int64_t>(__ldcg(labels + r)) * d + c]);
+      const T* wl = W + static_cast<int64_t>(__ldcg(labels + r)) * d + c;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (c + k < d) x[k] = co.x * x[k] - co.y * static_cast<float>(wl[k]);
     }
-    dH[static_cast<int64_t>(__ldcg(rows + r)) * d + c] = static_cast<T>(x);
+    store4(dH + row * d + c, x, c, d);
   }
 }
 
@@ -1139,12 +1155,13 @@ cudaError_t run_head(const HeadShape& s, const T* H, const T* W, const void* lab
     p.W = W;
     p.out = dH;
     cudaError_t e2 = run_gemm<DH, PLANES>(p, mt * dt * pl.splits, st);
-    if (e2 == cudaSuccess && i + 1 == pl.pieces && pl.splits > 1)
-      e2 = lm_launch(true, head_join_kernel<T>,
-                  dim3((s.d + 255) / 256, static_cast<unsigned>(std::min<int64_t>(s.N, 4096))), 256, 0, st,
-                  static_cast<const HeadState*>(state), only_retry, reinterpret_cast<const float*>(ws + pl.o_acc),
-                  pl.splits, pl.n_pad, pl.ldacc, s.d, static_cast<const int*>(rows), p.coef,
-                  static_cast<const int*>(lab), W, dH);
+    if (e2 == cudaSuccess && i + 1 == pl.pieces && pl.splits > 1) {
+      const unsigned gx = static_cast<unsigned>((s.d + 4 * kJoinThreads - 1) / (4 * kJoinThreads));
+      const unsigned gy = static_cast<unsigned>(std::min<int64_t>(s.N, std::max<int64_t>(1, kJoinBlocks / gx)));
+      e2 = lm_launch(true, head_join_kernel<T>, dim3(gx, gy), kJoinThreads, 0, st, static_cast<const HeadState*>(state),
+                     only_retry, reinterpret_cast<const float*>(ws + pl.o_acc), pl.splits, pl.n_pad, pl.ldacc, s.d,
+                     static_cast<const int*>(rows), p.coef, static_cast<const int*>(lab), W, dH);
+    }
     return e2;
   };
 
