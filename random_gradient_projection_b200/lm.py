@@ -68,15 +68,10 @@ def _tensor(x, what: str, dev: int, shape=None, dtypes=None):
         raise ValueError(f"{what}: need a torch tensor, got {type(x).__name__}")
     if dtypes is not None and x.dtype not in dtypes:
         raise ValueError(f"{what}: need one of {[str(t) for t in dtypes]}, got {x.dtype}")
-    if shape is not None:
+    if shape is not None and x.shape != shape:
         got = x.shape
-        ok = len(got) == len(shape)
-        if ok:
-            for want, size in zip(shape, got):
-                if want is not None and want != size:
-                    ok = False
-        if not ok:
-            raise ValueError(f"{what}: need shape {tuple('any' if s is None else s for s in shape)}, got {tuple(got)}")
+        if len(got) != len(shape) or any(w is not None and w != n for w, n in zip(shape, got)):
+            raise ValueError(f"{what}: need shape {tuple('any' if w is None else w for w in shape)}, got {tuple(got)}")
     if not x.is_contiguous():
         raise ValueError(f"{what}: need a contiguous tensor, got strides {x.stride()}")
     if x.get_device() != dev or not x.is_cuda:
