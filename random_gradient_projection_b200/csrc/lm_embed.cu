@@ -628,22 +628,26 @@ __global__ void __launch_bounds__(32 * kJoinWarps) segment_join_kernel(const Seg
   }
 }
 
-// sq[b] = sum of the slots of sample b over all tiles, in a fixed order.
-constexpr int kSumThreads = 1024;
-__global__ void __launch_bounds__(kSumThreads) sample_sums_kernel(const float* slots, int n, int T, int tiles, float* sq) {
+// sq[b] = sum of the slots of sample b over all tiles, in a fixed order.  A sample with many slots is
+// summed by a cluster of CTAs, whose sums its first one adds.
+constexpr int kSumThreads = 1024, kSumCluster = 8;
+__global__ void __launch_bounds__(kSumThreads) sample_sums_kernel(const float* slots, int n, int T, int tiles, int parts,
+                                                                  float* sq) {
   ptx::griddep_wait();
-  __shared__ float red[kSumThreads / 32];
+  __shared__ float red[kSumThreads / 32], sum;
+  const int b = blockIdx.x / parts, part = blockIdx.x % parts;
   float s = 0.0f;
-  const float* q = slots + static_cast<size_t>(blockIdx.x) * T;
+  const float* q = slots + static_cast<size_t>(b) * T;
   const int64_t total = static_cast<int64_t>(T) * tiles;
-  for (int64_t i0 = threadIdx.x; i0 < total; i0 += 8 * kSumThreads) {   // eight in flight
+  const int64_t end = total * (part + 1) / parts;
+  for (int64_t i0 = total * part / parts + threadIdx.x; i0 < end; i0 += 8 * kSumThreads) {   // eight in flight
     float x[8];
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       const int64_t i = i0 + u * kSumThreads;
       // (64-bit divisions would take longer than the loads)
       const int64_t tile = total <= 0xffffffffll ? static_cast<uint32_t>(i) / static_cast<uint32_t>(T) : i / T;
-      x[u] = i < total ? __ldcg(q + tile * n + (i - tile * T)) : 0.0f;
+      x[u] = i < end ? __ldcg(q + tile * n + (i - tile * T)) : 0.0f;
     }
 #pragma unroll
     for (int u = 0; u < 8; ++u) s += x[u];
@@ -653,8 +657,40 @@ __global__ void __launch_bounds__(kSumThreads) sample_sums_kernel(const float* s
   __syncthreads();
   if (threadIdx.x < 32) {
     s = warp_sum(red[threadIdx.x]);
-    if (threadIdx.x == 0) sq[blockIdx.x] = s;
+    if (threadIdx.x == 0) {
+      sum = s;
+      if (parts == 1) sq[b] = s;
+    }
   }
+  if (parts == 1) return;
+  __syncthreads();
+  ptx::cluster_sync();   // every CTA's sum is there
+  if (part == 0 && threadIdx.x == 0) {
+    float tot = 0.0f;
+    for (int c = 0; c < parts; ++c) tot += __uint_as_float(ld_dsmem_u32(ptx::cluster_addr(&sum, c)));
+    sq[b] = tot;
+  }
+  __syncthreads();
+  ptx::cluster_sync();   // and none leaves before it has been read
+}
+
+cudaError_t launch_sums(const SegParams& p, int B, float* sq, cudaStream_t st) {
+  // one round of eight values a thread is enough for one CTA
+  const int parts = static_cast<int64_t>(p.T) * p.tiles > 8 * kSumThreads ? kSumCluster : 1;
+  if (static_cast<int64_t>(B) * parts > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(B) * parts);
+  cfg.blockDim = dim3(kSumThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute a[2];
+  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a[0].val.programmaticStreamSerializationAllowed = 1;
+  a[1].id = cudaLaunchAttributeClusterDimension;
+  a[1].val.clusterDim.x = parts;
+  a[1].val.clusterDim.y = a[1].val.clusterDim.z = 1;
+  cfg.attrs = a;
+  cfg.numAttrs = parts > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, sample_sums_kernel, static_cast<const float*>(p.slots), p.n, p.T, p.tiles, parts, sq);
 }
 
 int tiles_of(int d) { return (d + 255) / 256; }
@@ -695,9 +731,7 @@ cudaError_t run_sqnorms(const SegParams& p, int B, const TG* G, float* sq, cudaS
   cudaError_t e = lm_launch(false, segment_kernel<TG, VEC, true>, dim3(blocks), 32 * kSegWarps, 0, st, p, G);
   if (e == cudaSuccess)
     e = lm_launch(true, segment_join_kernel<VEC, true>, dim3(join_blocks(p)), 32 * kJoinWarps, 0, st, p);
-  if (e == cudaSuccess)
-    e = lm_launch(true, sample_sums_kernel, dim3(B), kSumThreads, 0, st, static_cast<const float*>(p.slots), p.n, p.T,
-                  p.tiles, sq);
+  if (e == cudaSuccess) e = launch_sums(p, B, sq, st);
   return e;
 }
 

@@ -843,12 +843,32 @@ __global__ void __launch_bounds__(128) head_gather_kernel(const T* H, int d, int
 }
 
 // A copy of W that the tensor maps can address: rows padded to a multiple of eight, or three
-// planes of an fp32 W.
+// planes of an fp32 W.  Four columns a thread where W's rows allow it (10007 x 764 fp32: 13 us, 20 a column at a time).
 template <class T, int PLANES>
 __global__ void __launch_bounds__(128) head_weights_kernel(const T* W, int d, __nv_bfloat16* Wc, int plane) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const int64_t r = blockIdx.x;
+  if (PLANES == 3 && d % 4 == 0) {
+    for (int c = 4 * threadIdx.x; c < plane; c += 512) {
+      float x[4] = {0.f, 0.f, 0.f, 0.f};
+      if (c < d) {
+        const float4 y = *reinterpret_cast<const float4*>(W + r * d + c);
+        x[0] = y.x, x[1] = y.y, x[2] = y.z, x[3] = y.w;
+      }
+#pragma unroll
+      for (int k = 0; k < PLANES; ++k) {
+        alignas(8) __nv_bfloat16 b[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          b[e] = __float2bfloat16_rn(x[e]);
+          x[e] -= __bfloat162float(b[e]);
+        }
+        *reinterpret_cast<uint2*>(Wc + (r * PLANES + k) * plane + c) = *reinterpret_cast<const uint2*>(b);
+      }
+    }
+    return;
+  }
   for (int c = threadIdx.x; c < plane; c += 128) {
     float x = c < d ? static_cast<float>(W[r * d + c]) : 0.0f;
 #pragma unroll
