@@ -479,7 +479,8 @@ GRAPE_API int grape_embed_grad(const void* order, int32_t B, int32_t T, int32_t 
  *             large N), for fp32 or d % 8 != 0 a laid-out copy of W, and fp32 sums of dH where it
  *             is summed in pieces
  * All sums are fp32; with bf16 inputs the logits' gradient is rounded to bf16 before the second
- * products, with fp32 inputs products keep 24 bits.  If a bounded device-side wait gives up,
+ * products, with fp32 inputs products keep 24 bits (of finite entries up to 3.38e38: others give
+ * NaN in the products they enter).  If a bounded device-side wait gives up,
  * every loss is NaN.  N <= 2^30, N * vocab / 65536 < 2^31. */
 GRAPE_API int grape_head_loss_bytes(int64_t N, int32_t d, int32_t vocab, int32_t dtype, int32_t want_dH,
                                     int32_t want_dW, uint64_t* bytes);

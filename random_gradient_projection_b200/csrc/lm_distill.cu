@@ -168,8 +168,9 @@ __device__ __forceinline__ float unit_max(const uint4& r, __nv_bfloat16) {
   return fmaxf(__bfloat162float(m.x), __bfloat162float(m.y));
 }
 // A unit of nothing but -inf.
-__device__ __forceinline__ uint4 unit_none(float) { return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u); }
-__device__ __forceinline__ uint4 unit_none(__nv_bfloat16) { return make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u); }
+__device__ __forceinline__ uint4 unit_of(uint32_t w) { return make_uint4(w, w, w, w); }
+__device__ __forceinline__ uint4 unit_none(float) { return unit_of(0xff800000u); }
+__device__ __forceinline__ uint4 unit_none(__nv_bfloat16) { return unit_of(0xff80ff80u); }
 
 struct DistillParams {
   const void* idx;
@@ -360,8 +361,9 @@ __global__ void __launch_bounds__(THREADS, MINB) distill_kernel(const DistillPar
 // after which a chunk is stored and its slot loaded with the next row's data.  So memory does not wait for the
 // exponentials (two per element: for bf16 their unit alone takes 0.8 of the row's time on the bus)
 // nor for the reductions.  Bound by instruction issue, next to memory: 4096 x 50265 bf16 takes 174 us
-// (4.7 TB/s), 8192 x 128000 799 (5.3 TB/s), 4096 x 50265 fp32 290 (5.7 TB/s).  A row longer than the ring has its first chunks loaded twice, the
-// second time from L2; otherwise DRAM and L2 see every logit once and every gradient once.
+// (4.7 TB/s), 8192 x 128000 799 (5.3 TB/s), 4096 x 50265 fp32 290 (5.7 TB/s).  A row longer than the
+// ring has its first chunks loaded twice, the second time from L2; otherwise DRAM and L2 see every
+// logit once and every gradient once.
 // Four warps work on the teacher's entries: they prepare the next row's while a row is summed, and put
 // their mass into each finished chunk before it is stored.  Two threads issue the copies, each those
 // of every other slot: waiting until a slot has been read out takes a microsecond, which one thread
