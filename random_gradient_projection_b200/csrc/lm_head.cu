@@ -8,7 +8,7 @@
 // The contractions run on one warp-specialised kernel, head_gemm_kernel<EPI, PLANES>:
 //
 //   STATS  z over the whole vocabulary, reduced in the epilogue to a maximum and a sum of
-//          exponentials per row and tile (and the label's logit)
+//          exponentials per row and tile, and the label's logit beside them
 //   GRAD   z again for one piece of the vocabulary; the epilogue writes g for the piece
 //   EXP    z once for one piece; the epilogue writes e_nv = exp(z_nv - r_n) and its row sums,
 //          with a reference r_n that is known beforehand
@@ -26,8 +26,12 @@
 // and the label's own logit, one short dot product per row, is a reference r_n that keeps every
 // e_nv at most exp(l_n) and s_n at least 1.  So EXP overflows only where a row's loss passes 60;
 // an epilogue that sees this sets `retry`, and the two-pass kernels, which are launched behind
-// and otherwise leave at once, compute the call anew.  (The label's column is left out of e and of
-// the sum, so that 1 - p_n = s'_n / s_n and l_n = log1p(s'_n / e_label) stay exact for p_n near 1.)
+// and otherwise leave at once, compute the call anew.
+//
+// Both ways leave the label's column out of the sum s'_n, so that what is small for a row that is
+// sure of its label never is a difference of large numbers: 1 - p_n = s'_n / s_n with s_n = s'_n +
+// e_label, l_n = log1p(s'_n / e_label), and g's entry at the label is -w_n s'_n / s_n (from p_n - 1
+// it would be off by 2^-24 of the largest logit, all of it at 1 - p_n = 1e-6).
 //
 // Rows without a loss (label outside [0, V), or weight 0) are dropped first: where there are any,
 // the live rows are gathered in order into a compact H, so masked rows cost nothing, and whatever
@@ -126,10 +130,10 @@ struct HeadGemm {
   int v0, V, d;         // first vocabulary row of the piece; sizes
   int64_t n_pad;        // rows of the compact buffers
   const int* labels;    // compact rows
-  const float* weights;
-  const float* lse;     // GRAD
-  const float* ref;     // EXP: r_n
-  float2* parts;        // STATS: [tile][n_pad] (maximum, sum of exponentials); EXP: (sum, unused)
+  const float* ref;     // EXP: r_n; GRAD: the row's largest logit
+  const float2* scale;  // GRAD: w / s and w s' / s
+  float2* parts;        // STATS: [tile][n_pad] (maximum, sum of exponentials), the label's column
+                        // left out; EXP: (sum, unused)
   float* target;        // STATS: the label's logit; EXP: less r_n
   __nv_bfloat16* g;     // GRAD, EXP: [n_pad][ldg]
   int64_t ldg;
@@ -468,7 +472,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (label >= col0 && label < col0 + kCols) {
 #pragma unroll
             for (int j = 0; j < kCols; ++j)
-              if (label == col0 + j) p.target[row] = v[j];
+              if (label == col0 + j) {
+                p.target[row] = v[j];
+                v[j] = -INFINITY;   // left out of the sums
+              }
           }
           float m = v[0];
 #pragma unroll
@@ -479,8 +486,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int j = 0; j < kCols; ++j) s += ex2((v[j] - r) * kLog2e);
           part = make_float2(m, s);
         } else {
-          const float w = EPI == GRAD && live ? __ldcg(p.weights + row) : 1.0f;
-          const float r = live ? __ldcg((EPI == GRAD ? p.lse : p.ref) + row) : 0.0f;
+          const float2 w = EPI == GRAD && live ? __ldcg(p.scale + row) : make_float2(1.0f, 0.0f);
+          const float r = live ? __ldcg(p.ref + row) : 0.0f;
           if (EPI == EXP && label >= col0 && label < col0 + kCols) {
 #pragma unroll
             for (int j = 0; j < kCols; ++j)
@@ -492,11 +499,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               }
           }
 #pragma unroll
-          for (int j = 0; j < kCols; ++j) v[j] = w * ex2((v[j] - r) * kLog2e);
+          for (int j = 0; j < kCols; ++j) v[j] = w.x * ex2((v[j] - r) * kLog2e);
           if (EPI == GRAD && label >= col0 && label < col0 + kCols) {
 #pragma unroll
             for (int j = 0; j < kCols; ++j)
-              if (label == col0 + j) v[j] -= w;
+              if (label == col0 + j) v[j] = -w.y;
           }
           if (!live || left < kCols) {   // rows and columns that only fill up the tile
 #pragma unroll
@@ -881,12 +888,12 @@ __global__ void __launch_bounds__(128) head_weights_kernel(const T* W, int d, __
 }
 
 // The losses, from the rows' partial sums, 32 rows per CTA: eight threads share a row's parts, eight
-// loads of each in flight, joined in a fixed order.  After STATS (EXPS false): lse and loss.  After
-// EXP: loss, and the coefficients of dH.
+// loads of each in flight, joined in a fixed order.  After STATS (EXPS false): loss, the row's largest
+// logit and the coefficients of g (w / s, w s' / s).  After EXP: loss, and the same coefficients of dH.
 template <bool EXPS>
 __global__ void __launch_bounds__(256) head_loss_kernel(const HeadState* state, int only_retry, const float2* parts,
                                                         int slots, int64_t n_pad, const float* target,
-                                                        const float* weights, const int* rows, float* lse,
+                                                        const float* weights, const int* rows, float* top,
                                                         float2* coef, float* loss) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
@@ -940,9 +947,13 @@ __global__ void __launch_bounds__(256) head_loss_kernel(const HeadState* state, 
       s = 0.0f;
 #pragma unroll
       for (int k = 0; k < 8; ++k) join(red[k][lane].x, red[k][lane].y);
-      lse[row] = m + logf(s);
-      // log(s) - (target - m) rather than lse - target: the difference of the two large ones is exact
-      x = w * (logf(s) - (t - m));
+      // the label's term joins the others', each relative to the largest logit
+      const float mm = fmaxf(m, t), el = ex2((t - mm) * kLog2e);
+      s *= ex2((m - mm) * kLog2e);
+      const float inv = 1.0f / (s + el);
+      top[row] = mm;
+      coef[row] = make_float2(w * inv, w * (s * inv));
+      x = w * (t >= m ? log1pf(s) : logf(s + el) - (t - mm));   // (t >= m: el = 1)
     }
     if (__ldcg(&state->err)) x = __int_as_float(0x7fc00000);
     loss[__ldcg(rows + row)] = x;
@@ -1005,7 +1016,7 @@ struct HeadPlan {
   bool acc;                // DH goes through fp32 memory
   int64_t ldacc;
   bool one_pass;           // EXP
-  size_t o_rows, o_labels, o_weights, o_lse, o_coef, o_target, o_parts, o_H, o_W, o_g, o_acc, bytes;
+  size_t o_rows, o_labels, o_weights, o_ref, o_coef, o_target, o_parts, o_H, o_W, o_g, o_acc, bytes;
 
   explicit HeadPlan(const HeadShape& s) {
     planes = s.dtype == GRAPE_F32 ? 3 : 1;
@@ -1041,9 +1052,9 @@ struct HeadPlan {
     o_rows = take(np * 4);
     o_labels = take(np * 4);
     o_weights = take(np * 4);
-    o_lse = take(np * 4);
+    o_ref = take(np * 4);
     o_target = take(np * 4);
-    o_coef = take(one_pass ? np * 8 : 0);
+    o_coef = take(np * 8);
     o_parts = take(np * slots * 8);
     o_H = take(np * plane * planes * 2);
     o_W = take(copy_W ? static_cast<size_t>(s.V) * plane * planes * 2 : 0);
@@ -1070,7 +1081,7 @@ cudaError_t run_head(const HeadShape& s, const T* H, const T* W, const void* lab
   int* rows = reinterpret_cast<int*>(ws + pl.o_rows);
   int* lab = reinterpret_cast<int*>(ws + pl.o_labels);
   float* wgt = reinterpret_cast<float*>(ws + pl.o_weights);
-  float* lse = reinterpret_cast<float*>(ws + pl.o_lse);
+  float* ref = reinterpret_cast<float*>(ws + pl.o_ref);
   float* target = reinterpret_cast<float*>(ws + pl.o_target);
   float2* parts = reinterpret_cast<float2*>(ws + pl.o_parts);
   __nv_bfloat16* Hc = reinterpret_cast<__nv_bfloat16*>(ws + pl.o_H);
@@ -1080,7 +1091,7 @@ cudaError_t run_head(const HeadShape& s, const T* H, const T* W, const void* lab
   const int wide = pl.plane * PLANES;
   const int64_t gw = static_cast<int64_t>(pl.piece) * PLANES;
 
-  float2* coef = pl.one_pass ? reinterpret_cast<float2*>(ws + pl.o_coef) : nullptr;
+  float2* coef = reinterpret_cast<float2*>(ws + pl.o_coef);
   const int direct = PLANES == 1 && !pl.copy_W;   // H itself can be an operand when every row is live
 
   if (s.N == 0) return dW ? cudaMemsetAsync(dW, 0, static_cast<size_t>(s.V) * s.d * sizeof(T), st) : cudaSuccess;
@@ -1092,7 +1103,7 @@ cudaError_t run_head(const HeadShape& s, const T* H, const T* W, const void* lab
   if (e == cudaSuccess) {
     auto gather = [&](auto kernel) {
       return lm_launch(!few, kernel, dim3(static_cast<unsigned>(pl.n_pad)), 128, 0, st, H, s.d, s.N, state, rows, Hc,
-                       pl.plane, dH, direct, W, lab, pl.one_pass ? lse : nullptr,
+                       pl.plane, dH, direct, W, lab, pl.one_pass ? ref : nullptr,
                        FewRows{labels, id_bytes, s.V, weights, wgt, loss});
     };
     e = few ? gather(head_gather_kernel<T, PLANES, true>) : gather(head_gather_kernel<T, PLANES, false>);
@@ -1120,8 +1131,8 @@ cudaError_t run_head(const HeadShape& s, const T* H, const T* W, const void* lab
   base.d = s.d;
   base.n_pad = pl.n_pad;
   base.labels = lab;
-  base.weights = wgt;
-  base.lse = base.ref = lse;
+  base.ref = ref;
+  base.scale = coef;
   base.parts = parts;
   base.target = target;
   base.g = g;
@@ -1152,7 +1163,7 @@ cudaError_t run_head(const HeadShape& s, const T* H, const T* W, const void* lab
     auto go = [&](auto kernel) {
       return lm_launch(true, kernel, grid, 256, 0, st, static_cast<const HeadState*>(state), only_retry,
                     static_cast<const float2*>(parts), pl.slots, pl.n_pad, static_cast<const float*>(target),
-                    static_cast<const float*>(wgt), static_cast<const int*>(rows), lse, coef, loss);
+                    static_cast<const float*>(wgt), static_cast<const int*>(rows), ref, coef, loss);
     };
     return exps ? go(head_loss_kernel<true>) : go(head_loss_kernel<false>);
   };
