@@ -457,8 +457,9 @@ GRAPE_API int grape_embed_sqnorms(const void* order, int32_t B, int32_t T, int32
                                   float* sqnorms, void* stream);
 
 /* grad = sum_i weights[i] G_i, with G_i as above: vocab x d fp32, every row written (zero
- * where no token fell).  weights: B floats (the clip factors c_i), NULL for 1.  Sums are
- * fp32 in a fixed order: the same inputs give the same bits. */
+ * where no token fell).  weights: B floats (the clip factors c_i), NULL for 1; a sample of weight 0
+ * adds nothing and its Gout is not read (it may hold NaN).  Sums are fp32 in a fixed order: the
+ * same inputs give the same bits. */
 GRAPE_API int grape_embed_grad(const void* order, int32_t B, int32_t T, int32_t vocab, int32_t d,
                                const void* Gout, int32_t dtype, double scale, const float* weights,
                                void* workspace, float* grad, void* stream);

@@ -462,7 +462,9 @@ __global__ void __launch_bounds__(32 * kSegWarps) segment_kernel(const SegParams
   }
   const int count = __popc(__ballot_sync(0xffffffffu, tok < p.vocab));   // dropped items are last
   const int sample = NORMS || p.weights ? pos / p.T : 0;
-  const float w = p.scale * (!NORMS && p.weights && lane < count ? __ldg(p.weights + sample) : 1.0f);
+  const float c = !NORMS && p.weights && lane < count ? __ldg(p.weights + sample) : 1.0f;
+  const float w = p.scale * c;
+  const uint32_t out = NORMS ? 0u : __ballot_sync(0xffffffffu, c == 0.0f);   // their rows are not read
   // does the run of the first item begin earlier, does that of the last item go on?
   bool head = false, tail = false;
   if (count > 0) {
@@ -491,7 +493,7 @@ __global__ void __launch_bounds__(32 * kSegWarps) segment_kernel(const SegParams
 #pragma unroll
     for (int k = 0; k < kSegAhead; ++k) {
       const int row = __shfl_sync(0xffffffffu, pos, min(j0 + k, 31));
-      if (j0 + k < count) x[k].load(G + static_cast<size_t>(row) * p.d, col, p.d);
+      if (j0 + k < count && !((out >> (j0 + k)) & 1u)) x[k].load(G + static_cast<size_t>(row) * p.d, col, p.d);
     }
 #pragma unroll
     for (int k = 0; k < kSegAhead; ++k) {
@@ -499,10 +501,12 @@ __global__ void __launch_bounds__(32 * kSegWarps) segment_kernel(const SegParams
       const float wj = __shfl_sync(0xffffffffu, w, min(j, 31));
       const int tj = __shfl_sync(0xffffffffu, tok, min(j, 31));
       if (j < count) {
-        float f[8];
-        x[k].get(f);
+        if (!((out >> j) & 1u)) {
+          float f[8];
+          x[k].get(f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] = fmaf(wj, f[i], acc[i]);
+          for (int i = 0; i < 8; ++i) acc[i] = fmaf(wj, f[i], acc[i]);
+        }
         if ((ends >> j) & 1u) {
           if (head) {
             store8(part_at(p, chunk, 0, tile, lane), acc);
