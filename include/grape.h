@@ -222,7 +222,8 @@ GRAPE_API int grape_set_norm_method(grape_ctx* ctx, int32_t method);
  * takes the same c_i (grape_embed_grad).
  * grape_set_extra_sqnorms: the device address of B floats that every following step and
  *   accumulation adds to its n_i^2 (read when the step's work runs, so a caller refills the
- *   buffer for each step, in stream order); NULL (the default) adds nothing.  Graphs captured
+ *   buffer for each step, in stream order); NULL (the default) adds nothing.  The noise of such a
+ *   parameter's clipped sum is the caller's: the library adds noise to its own S_l.  Graphs captured
  *   with another address are dropped.  grape_sqnorms is not affected.
  * grape_clip_ptr: device address of the B clip factors c_i of the last step or accumulation
  *   (library-owned, rewritten by the next one).
@@ -474,7 +475,10 @@ GRAPE_API int grape_embed_grad(const void* order, int32_t B, int32_t T, int32_t 
  *             no loss: its loss and dH are 0, and its H is not read (it may hold NaN)
  *  weights    N floats (a token's share of its sample's loss, a clip factor), NULL for 1
  *  loss       N floats
- *  dH, dW     N x d and vocab x d in dtype, or NULL: not computed
+ *  dH, dW     N x d and vocab x d in dtype, or NULL: not computed.  dW is the sum over all rows: no
+ *             call gives a sample's norm of it, so a head that is trained under the per-sample
+ *             clip is a layer of the stack instead (and a head tied to the embedding table has a share in
+ *             the table's gradient that grape_embed_sqnorms and grape_embed_grad do not hold)
  *  workspace  grape_head_loss_bytes bytes: the live rows of H, 8 N vocab / 256 bytes of partial
  *             sums, one piece of the logits' gradient (at most 256 MiB, or 4096 columns for a
  *             large N), for fp32 or d % 8 != 0 a laid-out copy of W, and fp32 sums of dH where it
