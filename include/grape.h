@@ -223,8 +223,9 @@ GRAPE_API int grape_set_norm_method(grape_ctx* ctx, int32_t method);
  * grape_set_extra_sqnorms: the device address of B floats that every following step and
  *   accumulation adds to its n_i^2 (read when the step's work runs, so a caller refills the
  *   buffer for each step, in stream order); NULL (the default) adds nothing.  The noise of such a
- *   parameter's clipped sum is the caller's: the library adds noise to its own S_l.  Graphs captured
- *   with another address are dropped.  grape_sqnorms is not affected.
+ *   parameter's clipped sum is the caller's: the library adds noise to its own S_l.  A captured
+ *   step (grape_set_graph) is replayed with the address that is set at the time.  grape_sqnorms is not
+ *   affected.
  * grape_clip_ptr: device address of the B clip factors c_i of the last step or accumulation
  *   (library-owned, rewritten by the next one).
  * Errors: GRAPE_EINVAL (NULL ctx or clip_dev, misaligned address). */

@@ -84,7 +84,8 @@ struct grape_ctx {
   bool fuse_adam = true;
   bool fuses_adam() const { return fuse_adam && path == GRAPE_PATH_TC && stores_R(); }
   // CUDA-graph replay of grape_step (grape_set_graph): one graph per set of A, Gout, W
-  // pointers; the first step with a set captures it, later ones replay it
+  // pointers, with or without extra norms; the first step with a set captures it, later ones
+  // replay it
   struct StepGraph {
     std::vector<const void*> A, G;
     std::vector<float*> W;
@@ -92,6 +93,8 @@ struct grape_ctx {
     cudaGraph_t graph = nullptr;
     cudaGraphExec_t exec = nullptr;
     cudaGraphNode_t gen_p = nullptr, adam = nullptr;
+    cudaGraphNode_t extra = nullptr;   // add_extra_sqnorms, where with_extra
+    bool with_extra = false;
     bool adam_fused = false;   // the Adam node is tc_aggregate_adam's
     uint64_t launches = 0, used = 0;
   };
@@ -368,15 +371,15 @@ int run_step(grape_ctx* ctx, const void* const* A, const void* const* G, float* 
 
 // grape_step through a CUDA graph (see StepGraph).  Capture records the same launches as
 // run_accumulate + run_apply, including their programmatic (PDL) dependencies, on a
-// library stream; every replay rewrites the two step-dependent kernels' arguments (P's
-// Philox key; the step and bias corrections of noise + Adam) and launches the graph on
-// the caller's stream.  P is generated on every replay, so one graph serves any step.
+// library stream; every replay rewrites the step-dependent kernels' arguments (P's
+// Philox key; the step and bias corrections of noise + Adam; the address of the extra norms)
+// and launches the graph on the caller's stream.  P is generated on every replay, so one graph serves any step.
 int step_graph(grape_ctx* ctx, const void* const* A, const void* const* G, float* const* W, int64_t step,
                cudaStream_t st) {
   const int L = ctx->sh.L;
   grape_ctx::StepGraph* hit = nullptr;
   for (auto& g : ctx->graphs) {
-    bool same = true;
+    bool same = g.with_extra == (ctx->extra_sq != nullptr);
     for (int l = 0; l < L && same; ++l) same = g.A[l] == A[l] && g.G[l] == G[l] && g.W[l] == W[l];
     if (same) {
       hit = &g;
@@ -395,6 +398,7 @@ int step_graph(grape_ctx* ctx, const void* const* A, const void* const* G, float
     g.A.assign(A, A + L);
     g.G.assign(G, G + L);
     g.W.assign(W, W + L);
+    g.with_extra = ctx->extra_sq != nullptr;
     ctx->graphs.push_back(g);
     hit = &ctx->graphs.back();
   }
@@ -437,14 +441,15 @@ int step_graph(grape_ctx* ctx, const void* const* A, const void* const* G, float
       cudaKernelNodeParams kp{};
       if (cudaGraphKernelNodeGetParams(nd, &kp) != cudaSuccess) continue;
       if (kp.func == gen_fn) hit->gen_p = nd;
+      if (kp.func == grape::add_extra_func()) hit->extra = nd;
       if (kp.func == grape::noise_adam_func() || kp.func == grape::tc_aggregate_adam_func()) {
         hit->adam = nd;
         hit->adam_fused = kp.func == grape::tc_aggregate_adam_func();
       }
     }
-    if (!hit->gen_p || !hit->adam) {
+    if (!hit->gen_p || !hit->adam || hit->with_extra != (hit->extra != nullptr)) {
       ctx->drop_graph(*hit);
-      return ctx->fail(GRAPE_ECUDA, "captured step graph lacks its P-generation or Adam node");
+      return ctx->fail(GRAPE_ECUDA, "captured step graph lacks its P-generation, Adam or extra-norm node");
     }
     hit->captured = true;
   }
@@ -458,6 +463,8 @@ int step_graph(grape_ctx* ctx, const void* const* A, const void* const* G, float
                                                             update_scalars(ctx, step, 0), ctx->clip)
                         : grape::noise_adam_set_node(hit->exec, hit->adam, sh, ctx->ws.data(),
                                                      update_scalars(ctx, step, 0), ctx->path == GRAPE_PATH_TC);
+  if (e == cudaSuccess && hit->with_extra)
+    e = grape::add_extra_set_node(hit->exec, hit->extra, sh, ctx->extra_sq, ctx->partials);
   if (e == cudaSuccess) e = cudaGraphLaunch(hit->exec, st);
   if (e != cudaSuccess) return ctx->cuda_fail(e, "graph replay");
   ctx->launches += hit->launches;
@@ -876,11 +883,7 @@ int grape_set_extra_sqnorms(grape_ctx* ctx, const float* sqnorms_dev) {
   if (!ctx) return set_global(GRAPE_EINVAL, "ctx must not be null");
   if (reinterpret_cast<uintptr_t>(sqnorms_dev) & 3u)
     return ctx->fail(GRAPE_EINVAL, "sqnorms_dev must be aligned to its element size");
-  if (sqnorms_dev != ctx->extra_sq) {   // captured graphs hold the other address
-    for (auto& g : ctx->graphs) ctx->drop_graph(g);
-    ctx->graphs.clear();
-  }
-  ctx->extra_sq = sqnorms_dev;
+  ctx->extra_sq = sqnorms_dev;   // (replays are given the address: see step_graph)
   return GRAPE_OK;
 }
 

@@ -70,6 +70,10 @@ cudaError_t simt_generate_P_set_node(cudaGraphExec_t exec, cudaGraphNode_t node,
 cudaError_t sum_partials(const StepShape& sh, const float* partials, float* sqnorms, cudaStream_t st);
 // Adds extra[i] to sample i's squared norm (its first partial slot), before the clip.
 cudaError_t add_extra_sqnorms(const StepShape& sh, const float* extra, float* partials, cudaStream_t st);
+const void* add_extra_func();
+// Rewrites the arguments of add_extra_sqnorms' node in an instantiated graph.
+cudaError_t add_extra_set_node(cudaGraphExec_t exec, cudaGraphNode_t node, const StepShape& sh, const float* extra,
+                               float* partials);
 cudaError_t finalize_clip(const StepShape& sh, const float* partials, float* norms, float* clip,
                           cudaStream_t st);
 cudaError_t simt_aggregate(const StepShape& sh, const LayerWs* ws, const LayerIo* io,

@@ -542,6 +542,22 @@ cudaError_t simt_backproject(const StepShape& sh, const LayerWs* ws, const Layer
 const void* noise_adam_func() { return reinterpret_cast<const void*>(noise_adam_kernel); }
 const void* simt_generate_P_func() { return reinterpret_cast<const void*>(generate_P_kernel); }
 
+const void* add_extra_func() { return reinterpret_cast<const void*>(add_extra_kernel); }
+
+cudaError_t add_extra_set_node(cudaGraphExec_t exec, cudaGraphNode_t node, const StepShape& sh, const float* extra,
+                               float* partials) {
+  cudaKernelNodeParams p{};
+  cudaError_t e = cudaGraphKernelNodeGetParams(node, &p);
+  if (e != cudaSuccess) return e;
+  StepShape a0 = sh;
+  const float* a1 = extra;
+  float* a2 = partials;
+  void* args[] = {&a0, &a1, &a2};
+  p.kernelParams = args;
+  p.extra = nullptr;
+  return cudaGraphExecKernelNodeSetParams(exec, node, &p);
+}
+
 cudaError_t noise_adam_set_node(cudaGraphExec_t exec, cudaGraphNode_t node, const StepShape& sh,
                                 const LayerWs* ws, const UpdateScalars& u, bool dR_bf16) {
   cudaKernelNodeParams p{};

@@ -472,7 +472,7 @@ class GrapeStep:
     def set_extra_sqnorms(self, sqnorms):
         """Squared norms (B floats on the device, or None) of parameters beside the stack, which
         every following step adds to its samples' before the clip.  The tensor is kept
-        referenced and read when a step runs."""
+        referenced and read when a step runs; it may be another one for each step."""
         _need(sqnorms, self.B * 4, 4, "sqnorms", True)
         grape_set_extra_sqnorms(self.ctx, sqnorms)
         self._extra_sqnorms = sqnorms

@@ -166,3 +166,37 @@ def test_distillation_feeds_a_layer_of_the_stack():
     got = torch.from_numpy(step.S(0)).double().cuda()
     assert float((got - S).norm() / S.norm()) <= 2e-2 and float(c.min()) < 1.0
     step.close()
+
+
+def test_graphs_are_kept_when_the_norms_lie_elsewhere_each_step():
+    """`set_extra_sqnorms(lm.embed_sqnorms(...))` of every step is another tensor: the captured step is
+    replayed on it all the same (capturing it anew each time took 249 us against 43)."""
+    B, T, d, A, G, W = stack(layers=8)
+    g = GrapeStep([(d, d)] * 8, r=128, C=1.0, sigma=0.0, seed=1, B=B, T=T)
+    g.set_graph(True)
+    pool = torch.rand(12, B, device="cuda") * 40.0
+
+    def run(steps, address):
+        took = []
+        for s in range(steps):
+            x = pool[address(s)]
+            t = time.perf_counter()
+            g.set_extra_sqnorms(x)
+            g.step(A, G, W, s)
+            took.append(time.perf_counter() - t)
+            torch.cuda.synchronize()
+            n = (g.sqnorms(A, G, s).double() + x).sqrt().cpu()
+            assert torch.allclose(torch.from_numpy(g.norms()).double(), n, rtol=1e-5)
+        return statistics.median(took)
+    run(3, lambda s: 0)
+    fixed, moving = run(24, lambda s: 0), run(24, lambda s: s % 12)
+    print(f"median host time of a step: fixed {fixed * 1e6:.0f} us, moving {moving * 1e6:.0f} us")
+    assert moving <= 1.7 * fixed
+    # and without the share, and with it again
+    for x in (None, pool[3], None, pool[5]):
+        g.set_extra_sqnorms(x)
+        g.step(A, G, W, 30)
+        torch.cuda.synchronize()
+        n = (g.sqnorms(A, G, 30).double() + (0.0 if x is None else x)).sqrt().cpu()
+        assert torch.allclose(torch.from_numpy(g.norms()).double(), n, rtol=1e-5)
+    g.close()
