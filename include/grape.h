@@ -423,8 +423,9 @@ GRAPE_API int grape_layer_sqnorms_static(const void* A, const void* Gout, int32_
  * reused as soon as the call's work is done, and two calls whose work may overlap need one
  * each.  Device pointers of matrices, workspaces and outputs are 16-byte aligned; ids,
  * weights and per-row vectors need the alignment of their elements.  Token numbers (ids, labels, teacher
- * indices) are int32 or int64: id_bytes is 4 or 8.  vocab lies in [1, 2^30], d in [1, 2^20].  A number outside [0, vocab) is no error:
- * it means "no token" as each call states.  Errors are reported through
+ * indices) are int32 or int64: id_bytes is 4 or 8.  vocab lies in [1, 2^30], d in [1, 2^20], and a scale
+ * is finite in fp32.  A token number outside [0, vocab) is no error: it means "no token" as each call
+ * states.  Errors are reported through
  * grape_global_error(): GRAPE_EINVAL (arguments), GRAPE_EUNSUPPORTED (not an sm_100a device,
  * or no tensor-map encoder in the driver), GRAPE_ECUDA. */
 
@@ -507,7 +508,7 @@ GRAPE_API int grape_head_loss(const void* H, const void* W, const void* labels, 
  *             Gout 0, whatever its logits hold.
  *  Gout       N x vocab, dtype; may be `logits` itself (overwritten in place) and must not
  *             overlap it otherwise
- * Statistics are fp32, Gout is rounded once.  N <= 2^31 - 1, temperature > 0. */
+ * Statistics are fp32, Gout is rounded once.  N <= 2^31 - 1, temperature in [2^-60, 2^60]. */
 GRAPE_API int grape_distill_loss(const void* logits, int32_t dtype, int64_t N, int32_t vocab,
                                  const void* indices, int32_t id_bytes, const void* values,
                                  int32_t value_dtype, int32_t K, const float* weights, double temperature,

@@ -111,7 +111,7 @@ int grape_embed(const void* table, int32_t table_dtype, const void* ids, int32_t
     if (const char* m = ids_problem(ids, id_bytes, n_ids, vocab)) return einval(m);
     if (d < 1 || d > kMaxWidth) return einval(kWidthRange);
     if (!dtype_ok(table_dtype) || !dtype_ok(out_dtype)) return einval("dtypes must be GRAPE_F32 or GRAPE_BF16");
-    if (!std::isfinite(scale)) return einval("scale must be finite");
+    if (!std::isfinite(static_cast<float>(scale))) return einval("scale must be finite in fp32");
     if (n_ids == 0) return GRAPE_OK;
     if (!table || !out) return einval("table and out must not be null");
     if (!aligned16(table) || !aligned16(out)) return einval("table and out must be 16-byte aligned");
@@ -151,7 +151,7 @@ int grape_embed_sqnorms(const void* order, int32_t B, int32_t T, int32_t vocab, 
   return guarded("grape_embed_sqnorms", [&]() -> int {
     if (const char* m = batch_problem(B, T, vocab, d)) return einval(m);
     if (!dtype_ok(dtype)) return einval("dtype must be GRAPE_F32 or GRAPE_BF16");
-    if (!std::isfinite(scale)) return einval("scale must be finite");
+    if (!std::isfinite(static_cast<float>(scale))) return einval("scale must be finite in fp32");
     if (!order || !aligned16(order) || !workspace || !aligned16(workspace))
       return einval("order and workspace must be 16-byte aligned device buffers");
     if (B > 0 && (!sqnorms || !aligned(sqnorms, 4))) return einval("sqnorms must not be null");
@@ -169,7 +169,7 @@ int grape_embed_grad(const void* order, int32_t B, int32_t T, int32_t vocab, int
   return guarded("grape_embed_grad", [&]() -> int {
     if (const char* m = batch_problem(B, T, vocab, d)) return einval(m);
     if (!dtype_ok(dtype)) return einval("dtype must be GRAPE_F32 or GRAPE_BF16");
-    if (!std::isfinite(scale)) return einval("scale must be finite");
+    if (!std::isfinite(static_cast<float>(scale))) return einval("scale must be finite in fp32");
     if (!order || !aligned16(order) || !workspace || !aligned16(workspace))
       return einval("order and workspace must be 16-byte aligned device buffers");
     if (!grad || !aligned16(grad)) return einval("grad must not be null and must be 16-byte aligned");
@@ -218,7 +218,8 @@ int grape_distill_loss(const void* logits, int32_t dtype, int64_t N, int32_t voc
     if (N < 0 || N > 0x7fffffff) return einval("N must lie in [0, 2^31 - 1]");
     if (vocab < 1 || vocab > kMaxVocab) return einval(kVocabRange);
     if (K < 1 || K > grape::kMaxTeacher) return einval("K must lie in [1, 1024]");
-    if (!(temperature > 0) || !std::isfinite(temperature)) return einval("temperature must be positive and finite");
+    // (so that log2(e) / temperature and temperature^2 are finite and normal in fp32)
+    if (!(temperature >= 0x1p-60 && temperature <= 0x1p60)) return einval("temperature must lie in [2^-60, 2^60]");
     if (N == 0) return GRAPE_OK;
     if (!logits || !indices || !values || !loss || !Gout)
       return einval("logits, indices, values, loss and Gout must not be null");

@@ -92,3 +92,25 @@ def test_a_student_near_its_hard_label(V, dt, offset):
     z.scatter_(1, idx, math.log(V * 1.65) + 11.0)
     z += offset
     check(z.to(dt), idx, torch.zeros(N, 1, device="cuda"), 1.0)
+
+
+@pytest.mark.parametrize("V", [4099, 20001])
+@pytest.mark.parametrize("tau", [2.0 ** -60, 2.0 ** -20, 2.0 ** 10])
+def test_temperatures_near_the_ends_of_their_range(V, tau):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(V + 2)
+    z = 3.0 * torch.randn(6, V, generator=g, device="cuda")
+    idx = torch.randint(V, (6, 5), generator=g, device="cuda")
+    idx[:, 0] = z.argmax(1)
+    check(z, idx, torch.randn(6, 5, generator=g, device="cuda"), tau)
+
+
+@pytest.mark.parametrize("V", [4099, 20001])
+def test_the_highest_temperature_is_the_uniform_distribution(V):
+    z = torch.randn(4, V, device="cuda")
+    idx = torch.tensor([[0, 1, 2, 3]] * 4, device="cuda")
+    tau = 2.0 ** 60
+    loss, G = lm.distill_loss(z, idx, torch.randn(4, 4, device="cuda"), temperature=tau)
+    want = torch.full_like(G, tau / V)
+    want[:, :4] -= tau / 4
+    assert loss.isfinite().all() and torch.allclose(G, want, rtol=1e-5)
