@@ -331,6 +331,12 @@ def grape_gaussian(seed: int, layer: int, step: int, stream_id: int, n: int, out
                                 _stream(stream)))
 
 
+# Sizes that ctypes would wrap are refused: 2**32 + 5 tokens are not 5.  (In line at each call: a
+# function for the comparison costs a small lookup 5 % of its time.)
+def _too_wide(*sizes):
+    raise ValueError(f"sizes {sizes}: one does not fit an int32")
+
+
 def grape_set_extra_sqnorms(ctx: int, sqnorms_dev):
     _check(lib().grape_set_extra_sqnorms(ctx, _ptr(sqnorms_dev)), ctx)
 
@@ -343,21 +349,29 @@ def grape_clip_ptr(ctx: int) -> int:
 
 def grape_embed(table, table_dtype: int, ids, id_bytes: int, n_ids: int, vocab: int, d: int, scale: float,
                 out_dtype: int, out, stream=None):
+    if not (-0x80000000 <= vocab <= 0x7fffffff and -0x80000000 <= d <= 0x7fffffff):
+        _too_wide(vocab, d)
     _check(lib().grape_embed(_ptr(table), table_dtype, _ptr(ids), id_bytes, n_ids, vocab, d, scale,
                              out_dtype, _ptr(out), _stream(stream)))
 
 
 def grape_embed_order_bytes(n_ids: int, vocab: int) -> int:
+    if not -0x80000000 <= vocab <= 0x7fffffff:
+        _too_wide(vocab)
     out = ctypes.c_uint64()
     _check(lib().grape_embed_order_bytes(n_ids, vocab, ctypes.byref(out)))
     return out.value
 
 
 def grape_embed_order(ids, id_bytes: int, n_ids: int, vocab: int, order, stream=None):
+    if not -0x80000000 <= vocab <= 0x7fffffff:
+        _too_wide(vocab)
     _check(lib().grape_embed_order(_ptr(ids), id_bytes, n_ids, vocab, _ptr(order), _stream(stream)))
 
 
 def grape_embed_workspace_bytes(B: int, T: int, vocab: int, d: int) -> int:
+    if min(B, T, vocab, d) < -0x80000000 or max(B, T, vocab, d) > 0x7fffffff:
+        _too_wide(B, T, vocab, d)
     out = ctypes.c_uint64()
     _check(lib().grape_embed_workspace_bytes(B, T, vocab, d, ctypes.byref(out)))
     return out.value
@@ -365,17 +379,23 @@ def grape_embed_workspace_bytes(B: int, T: int, vocab: int, d: int) -> int:
 
 def grape_embed_sqnorms(order, B: int, T: int, vocab: int, d: int, Gout, dtype: int, scale: float, workspace,
                         sqnorms, stream=None):
+    if min(B, T, vocab, d) < -0x80000000 or max(B, T, vocab, d) > 0x7fffffff:
+        _too_wide(B, T, vocab, d)
     _check(lib().grape_embed_sqnorms(_ptr(order), B, T, vocab, d, _ptr(Gout), dtype, scale, _ptr(workspace),
                                      _ptr(sqnorms), _stream(stream)))
 
 
 def grape_embed_grad(order, B: int, T: int, vocab: int, d: int, Gout, dtype: int, scale: float, weights,
                      workspace, grad, stream=None):
+    if min(B, T, vocab, d) < -0x80000000 or max(B, T, vocab, d) > 0x7fffffff:
+        _too_wide(B, T, vocab, d)
     _check(lib().grape_embed_grad(_ptr(order), B, T, vocab, d, _ptr(Gout), dtype, scale, _ptr(weights),
                                   _ptr(workspace), _ptr(grad), _stream(stream)))
 
 
 def grape_head_loss_bytes(N: int, d: int, vocab: int, dtype: int, want_dH: bool, want_dW: bool) -> int:
+    if not (-0x80000000 <= d <= 0x7fffffff and -0x80000000 <= vocab <= 0x7fffffff):
+        _too_wide(d, vocab)
     out = ctypes.c_uint64()
     _check(lib().grape_head_loss_bytes(N, d, vocab, dtype, int(want_dH), int(want_dW), ctypes.byref(out)))
     return out.value
@@ -383,12 +403,16 @@ def grape_head_loss_bytes(N: int, d: int, vocab: int, dtype: int, want_dH: bool,
 
 def grape_head_loss(H, W, labels, id_bytes: int, weights, N: int, d: int, vocab: int, dtype: int, workspace,
                     loss, dH=None, dW=None, stream=None):
+    if not (-0x80000000 <= d <= 0x7fffffff and -0x80000000 <= vocab <= 0x7fffffff):
+        _too_wide(d, vocab)
     _check(lib().grape_head_loss(_ptr(H), _ptr(W), _ptr(labels), id_bytes, _ptr(weights), N, d, vocab, dtype,
                                  _ptr(workspace), _ptr(loss), _ptr(dH), _ptr(dW), _stream(stream)))
 
 
 def grape_distill_loss(logits, dtype: int, N: int, vocab: int, indices, id_bytes: int, values, value_dtype: int,
                        K: int, weights, temperature: float, loss, Gout, stream=None):
+    if not (-0x80000000 <= vocab <= 0x7fffffff and -0x80000000 <= K <= 0x7fffffff):
+        _too_wide(vocab, K)
     _check(lib().grape_distill_loss(_ptr(logits), dtype, N, vocab, _ptr(indices), id_bytes, _ptr(values),
                                     value_dtype, K, _ptr(weights), temperature, _ptr(loss), _ptr(Gout),
                                     _stream(stream)))
