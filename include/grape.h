@@ -488,7 +488,7 @@ GRAPE_API int grape_embed_grad(const void* order, int32_t B, int32_t T, int32_t 
  * All sums are fp32; with bf16 inputs the logits' gradient is rounded to bf16 before the second
  * products, with fp32 inputs products keep 24 bits (of finite entries up to 3.38e38: others give
  * NaN in the products they enter).  If a bounded device-side wait gives up,
- * every loss is NaN.  N <= 2^30, N * vocab / 65536 < 2^31. */
+ * every loss is NaN, and dH and dW do not count.  N <= 2^30, N * vocab / 65536 < 2^31. */
 GRAPE_API int grape_head_loss_bytes(int64_t N, int32_t d, int32_t vocab, int32_t dtype, int32_t want_dH,
                                     int32_t want_dW, uint64_t* bytes);
 GRAPE_API int grape_head_loss(const void* H, const void* W, const void* labels, int32_t id_bytes,
@@ -508,7 +508,8 @@ GRAPE_API int grape_head_loss(const void* H, const void* W, const void* labels, 
  *             Gout 0, whatever its logits hold.
  *  Gout       N x vocab, dtype; may be `logits` itself (overwritten in place) and must not
  *             overlap it otherwise
- * Statistics are fp32, Gout is rounded once.  N <= 2^31 - 1, temperature in [2^-60, 2^60]. */
+ * Statistics are fp32, Gout is rounded once.  If a bounded device-side wait gives up, the loss of every
+ * row whose Gout it may have spoilt is NaN.  N <= 2^31 - 1, temperature in [2^-60, 2^60]. */
 GRAPE_API int grape_distill_loss(const void* logits, int32_t dtype, int64_t N, int32_t vocab,
                                  const void* indices, int32_t id_bytes, const void* values,
                                  int32_t value_dtype, int32_t K, const float* weights, double temperature,

@@ -622,14 +622,17 @@ __global__ void __launch_bounds__(RowCfg<MINB>::kBlock, MINB)
         bar_sync<kBarTeach, kTeachThreads>();
       if (t0 == 0) {
         const float* r = tred[j & 1];
-        p.loss[row] = *abort      ? __int_as_float(0x7fc00000)
-                      : loss_live ? gs * p.tau * 0.69314718055994531f * ((r[0] + r[1]) + (r[2] + r[3]))
-                                  : 0.0f;
+        p.loss[row] = loss_live ? gs * p.tau * 0.69314718055994531f * ((r[0] + r[1]) + (r[2] + r[3])) : 0.0f;
       }
       row = nrow;
       w = nw;
       ++j;
     }
+    // Where a wait gave up, a gradient may be missing or wrong in any of this CTA's rows, the finished
+    // ones included (their last chunks are stored late): none of their losses stands.  (This thread
+    // writes the losses, and every wait of the others is for chunks that have passed through here.)
+    if (t0 == 0 && *abort)
+      for (row = first; row < p.N; row += step) p.loss[row] = __int_as_float(0x7fc00000);
   } else {
     // ---------------- arithmetic ----------------
     uint32_t j = 0;
