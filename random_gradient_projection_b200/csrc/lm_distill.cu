@@ -348,10 +348,12 @@ __global__ void __launch_bounds__(THREADS, MINB) distill_kernel(const DistillPar
 // passes over the row's chunks: maximum and sum as they arrive, then the gradient, chunk by chunk,
 // after which a chunk is stored and its slot loaded with the next row's data.  So memory does not wait for the
 // exponentials (two per element: for bf16 their unit alone takes 0.8 of the row's time on the bus)
-// nor for the reductions.  Bound by instruction issue, next to memory: 4096 x 50265 bf16 takes 174 us
-// (4.7 TB/s), 8192 x 128000 799 (5.3 TB/s), 4096 x 50265 fp32 290 (5.7 TB/s).  A row longer than the
-// ring has its first chunks loaded twice, the second time from L2; otherwise DRAM and L2 see every
-// logit once and every gradient once.
+// nor for the reductions.  Bound by instruction issue (2.7 a cycle of an SM), next to memory: 4096 x
+// 50265 bf16 takes 170 us (4.8 TB/s), 8192 x 128000 850-870 (4.9 TB/s), 4096 x 50265 fp32 288-299
+// (5.6 TB/s).  A row longer than the ring has its first chunks loaded twice, the second time from
+// L2; otherwise DRAM and L2 see every logit once and every gradient once.
+// Rows are dealt out by their number, whatever their weights: where many have none, the CTA with the
+// most live rows decides (4096 x 50265 with 15 / 50 / 90 % of the rows masked at random: 167 / 140 / 98 us).
 // Four warps work on the teacher's entries: they prepare the next row's while a row is summed, and put
 // their mass into each finished chunk before it is stored.  Two threads issue the copies, each those
 // of every other slot: waiting until a slot has been read out takes a microsecond, which one thread
@@ -788,12 +790,13 @@ cudaError_t run_rows(const DistillParams& p, const void* logits, void* Gout, cud
 
 // Which kernel, from the bytes of a row (us at N = 8192, measured):
 //  - up to 32 KB, 128 threads a row and eight rows an SM, the part of a row beyond their registers
-//    coming from L2 a second time (bf16 V = 8192: 77 against 103 for the ring; V = 4000: 51 against 96);
-//  - beyond, the ring, with two CTAs on an SM up to 64 KB (bf16 V = 32000: 229 against 249 with one)
-//    and one from there on, with half as many threads again (bf16 V = 128000: 773, with 512 threads 820,
-//    and 891 with two; fp32 V = 32000: 349 against 368);
+//    coming from L2 a second time (bf16 V = 4000: 46 against 80 for the ring; V = 8192: 72 against 91; V =
+//    16000: 129 against 139; V = 20000, beyond: 153 against 161; V = 32000: 284 against 218);
+//  - beyond, the ring, with two CTAs on an SM up to 64 KB (bf16 V = 32000: 218 against 243 with one; bf16
+//    V = 50265, beyond: 168 at N = 4096 against 170) and one from there on, with half as many
+//    threads again (bf16 V = 128000: 861 against 921 with two; fp32 V = 32000: 354 against 380);
 //  - long rows with more than 128 teacher entries: 512 threads and two rows an SM, otherwise as
-//    the first (bf16 V = 128000: 1041).
+//    the first (bf16 V = 128000: 1100).
 constexpr int64_t kShortUpTo = 32768, kTwoUpTo = 65536;
 template <class T>
 cudaError_t pick(const DistillParams& p, const void* logits, void* Gout, cudaStream_t st) {

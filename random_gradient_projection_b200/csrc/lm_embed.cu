@@ -361,8 +361,8 @@ __global__ void __launch_bounds__(kSortThreads) embed_order_kernel(const void* i
 // and the last may go on in the chunks around, so their sums go to part[chunk][0] (a run that
 // began earlier) or part[chunk][1] (one that begins here), and a second, short launch adds those in
 // chunk order.  So a token that fills half the batch is spread over as many warps as any other.
-// Bound by memory: 16 x 512 tokens, d = 4096, vocab 32000, bf16: the gradient with its zero rows
-// 99 us (591 MB, 6.0 TB/s), the norms 17 us (67 MB, 4.0 TB/s).
+// Bound by memory: 16 x 512 tokens, d = 4096, vocab 32000, bf16: the gradient with its zero rows and
+// joins 102 us (591 MB, 5.8 TB/s), the norms with theirs 21 us (67 MB, 3.2 TB/s).
 struct SegParams {
   const int* positions;
   const int* tokens;
@@ -533,7 +533,9 @@ __global__ void __launch_bounds__(32 * kSegWarps) segment_kernel(const SegParams
 
 // The runs that begin in a chunk and go on in the next ones: their partial sums, added in a fixed
 // order.  A CTA looks at eight chunks, one per warp, in one 256-column tile.  A run over few chunks is
-// added by its warp; a longer one by all eight warps, an eighth of its chunks each.
+// added by its warp; a longer one by all eight warps, an eighth of its chunks each (from 4 / 16 / 64
+// chunks on, us: norms of 16 x 512 x 1024 14.3 / 12.9 / 12.9, gradient 33.3 / 33.3 / 35.6, gradient of 8 x
+// 8192 x 1024 68.2 / 68.2 / 70.6).
 constexpr int kJoinWarps = 8, kJoinAlone = 16;
 
 __device__ __forceinline__ void add_parts(const SegParams& p, int c0, int c1, int tile, int lane, float (&acc)[8]) {
@@ -700,8 +702,11 @@ cudaError_t launch_sums(const SegParams& p, int B, float* sq, cudaStream_t st) {
 int tiles_of(int d) { return (d + 255) / 256; }
 
 // Items per chunk: 32 (a lane each) once that gives every SM 16 warps, else 8, so that a short
-// batch still spreads over the machine.
-int chunk_items(int64_t n, int d) { return n * tiles_of(d) / 32 >= 148 * 16 ? 32 : 8; }
+// batch still spreads over the machine.  (8 against 32, us, norms and gradient: 1 x 512 x 256 10.0 and 5.7
+// / 13.4 and 8.8, 16 x 512 x 1024 12.9 and 33.3 / 16.5 and 31.6, 16 x 512 x 4096 29.3 and 106 / 21.2 and
+// 102, 8 x 8192 x 1024 60 and 94 / 43 and 68.)
+constexpr int kPlanSms = 148;   // of a B200 (workspaces are sized without asking a device)
+int chunk_items(int64_t n, int d) { return n * tiles_of(d) / 32 >= kPlanSms * 16 ? 32 : 8; }
 
 SegParams seg_params(const void* order, int B, int T, int vocab, int d, float scale, void* ws) {
   const int64_t n = static_cast<int64_t>(B) * T;
@@ -743,7 +748,7 @@ template <class TG, bool VEC>
 cudaError_t run_grad(SegParams p, const TG* G, cudaStream_t st) {
   const int64_t jobs = static_cast<int64_t>(p.chunks) * p.tiles;
   const unsigned blocks = static_cast<unsigned>((jobs + kSegWarps - 1) / kSegWarps);
-  const unsigned zero = static_cast<unsigned>(std::min<int64_t>((p.vocab + kSegWarps - 1) / kSegWarps, 148 * 8));
+  const unsigned zero = static_cast<unsigned>(std::min<int64_t>((p.vocab + kSegWarps - 1) / kSegWarps, kPlanSms * 8));
   p.seg_blocks = static_cast<int>(blocks);
   cudaError_t e = lm_launch(false, segment_kernel<TG, VEC, false>, dim3(blocks + zero), 32 * kSegWarps, 0, st, p, G);
   if (e == cudaSuccess && blocks > 0)

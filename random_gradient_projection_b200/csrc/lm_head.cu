@@ -26,7 +26,8 @@
 // and the label's own logit, one short dot product per row, is a reference r_n that keeps every
 // e_nv at most exp(l_n) and s_n at least 1.  So EXP overflows only where a row's loss passes 60;
 // an epilogue that sees this sets `retry`, and the two-pass kernels, which are launched behind
-// and otherwise leave at once, compute the call anew.
+// and otherwise leave at once, compute the call anew: one such row makes the whole call take 2.4 times
+// as long (8192 x 4096 x 32000: 3.5 -> 8.4 ms).
 //
 // Both ways leave the label's column out of the sum s'_n, so that what is small for a row that is
 // sure of its label never is a difference of large numbers: 1 - p_n = s'_n / s_n with s_n = s'_n +
@@ -34,9 +35,11 @@
 // it would be off by 2^-24 of the largest logit, all of it at 1 - p_n = 1e-6).
 //
 // Rows without a loss (label outside [0, V), or weight 0) are dropped first: where there are any,
-// the live rows are gathered in order into a compact H, so masked rows cost nothing, and whatever
+// the live rows are gathered in order into a compact H, so masked rows enter no product, and whatever
 // they hold (NaN included) reaches no sum.  The number of live rows is known on the device only;
-// every kernel reads it there.
+// every kernel reads it there.  (The plan - pieces, splits, one pass or two - and the workspace are
+// made for all N rows, so a call with few live ones fills the machine less well: 8192 x 1024 x
+// 32000 dH takes 1005 us, with half of the rows masked 540, with 90 % 278.)
 //
 // Precision.  bf16 inputs: products are exact in the tensor core and accumulate in fp32; g (or e) is
 // rounded once to bf16 as the operand of the second product (relative 2^-8 at most per element,
@@ -91,8 +94,13 @@ constexpr int kBoxOff = kBarOff + 1024;
 constexpr int kSmem = kBoxOff + kEpiWarps * kBox + 1024;   // + alignment slack
 static_assert(kBoxOff % 1024 == 0, "boxes are aligned");
 static_assert(kSmem <= 227 * 1024, "shared memory of an SM");
-constexpr int kSplitBlocks = 24;      // (a block takes about 0.1 us, joining the splits 3)
-constexpr int kGroupM = 8;            // row tiles that share a column of B tiles in L2
+// Blocks of 64 of a split of DH at least: a block is 8.4 MFLOP, 0.38 us at a pair's share of the
+// measured rate, and joining the splits takes 3 us.  (dH with 6 / 24 / 96, us: 64 x 256 x 1000 31 / 33 /
+// 33, 64 x 1024 x 32000 57 / 57 / 73, 512 x 1024 x 32000 88 / 88 / 98, 2048 x 1024 x 32000 255 / 246 / 261.)
+constexpr int kSplitBlocks = 24;
+// Row tiles that share a column of B tiles in L2 (4 / 8 / 16: 2048 x 1024 x 50265 399-421 / 395-400 /
+// 397 us, 8192 x 4096 x 32000 3536-3609 / 3464-3535 / 3481-3517).
+constexpr int kGroupM = 8;
 constexpr uint64_t kWaitLimitNs = 4000000000ull;
 constexpr uint64_t kDrainNs = 20000000ull;
 constexpr size_t kPieceBytes = size_t(256) << 20;
@@ -721,7 +729,8 @@ __global__ void __launch_bounds__(1024) head_rows_kernel(const void* labels, int
 // rows up to a whole tile; nothing where the products can read H itself (`direct` and every row
 // live).  Dropped rows of dH are zeroed.  ref (not null): the label's logit of each live row.
 // With few rows (FEW: at most kFewRows) there is no launch of head_rows_kernel before: every CTA counts
-// the live rows itself, and writes its own row's entry of what that kernel writes.
+// the live rows itself, and writes its own row's entry of what that kernel writes (512 x 256 x 1000: 35.8
+// us, with the launch 37.5; the two meet at 1024 rows, 38.4 and 38.8).
 constexpr int kFewRows = 1024, kFewPer = kFewRows / 128;
 struct FewRows {
   const void* labels;
@@ -961,8 +970,9 @@ __global__ void __launch_bounds__(256) head_loss_kernel(const HeadState* state, 
 }
 
 // dH from the splits of the vocabulary, added in order (and, after EXP, the coefficients applied).  A
-// thread takes four columns, eight splits' values in flight; at most kJoinBlocks CTAs, so that a
-// launch that leaves at once costs little (1000 rows of 1000: 8 us with a CTA a row).
+// thread takes four columns, eight splits' values in flight; at most kJoinBlocks CTAs, four an SM, so
+// that a launch that leaves at once costs little (512 x 1024 x 32000 with 148 / 592 / 2368: 106 / 88 / 85
+// us, 64 x 256 x 1000 33.6 / 33.2 / 33.2).
 constexpr int kJoinThreads = 128, kJoinBlocks = 592;
 template <class T>
 __global__ void __launch_bounds__(kJoinThreads) head_join_kernel(const HeadState* state, int only_retry,
@@ -1002,9 +1012,11 @@ __global__ void __launch_bounds__(kJoinThreads) head_join_kernel(const HeadState
 // ---- host ---------------------------------------------------------------------------------------
 
 // From this many multiplications (rows in whole tiles) x d x V on, dH alone takes one pass: the product
-// it saves is worth more than the launches behind it that leave at once, 2 us each (8.4e9: 79
-// against 84 us, 3.4e10 with 64 rows: 141 against 182; 2e9: 60 against 60).
+// it saves is worth more than the launches behind it that leave at once, 2 us each (one pass against
+// two, us: 256 x 256 x 30000, 2.0e9, 52 / 53; 512 x 512 x 16000, 4.2e9, 51 / 53; 512 x 512 x 32000 70 / 75;
+// 64 x 1024 x 128000, 3.4e10 in whole tiles, 153 / 191).
 constexpr double kOnePassWork = 4.0e9;
+constexpr int kPlanPairs = 74;         // pairs of SMs of a B200 (a plan is made without asking a device)
 
 struct HeadPlan {
   int planes, plane;       // bf16 planes of an operand; elements of a plane's row
@@ -1036,9 +1048,9 @@ struct HeadPlan {
     // kSplitBlocks blocks of 64 (of every kept product) each
     const int64_t out_tiles = n_pad / kTile * ((s.d + kTile - 1) / kTile);
     splits = 1;
-    if (s.dH && out_tiles > 0 && out_tiles < 74)
+    if (s.dH && out_tiles > 0 && out_tiles < kPlanPairs)
       splits = static_cast<int>(std::max<int64_t>(
-          1, std::min<int64_t>(74 / out_tiles, piece / kBK * (planes == 3 ? 6 : 1) / kSplitBlocks)));
+          1, std::min<int64_t>(kPlanPairs / out_tiles, piece / kBK * (planes == 3 ? 6 : 1) / kSplitBlocks)));
     acc = s.dH && (pieces > 1 || splits > 1);
     ldacc = (s.d + 3) / 4 * 4;
     size_t o = 256;

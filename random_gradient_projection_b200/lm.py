@@ -6,9 +6,11 @@ gradient per sample: its squared norm, which joins the layers' before the clip, 
 clipped sum.  Formulas and layouts are in include/grape.h.
 
 Every call checks its tensors and raises ValueError for a wrong size, type, device or
-stride before the library sees an address; outputs and workspaces come from torch's allocator
-on the stream the call runs on, so a call may be captured into a CUDA graph, and calls on
-different streams share nothing.
+stride before the library sees an address; what the library itself refuses (addresses off the
+16-byte rule, numbers outside their range) raises GrapeError.  Outputs and workspaces come from
+torch's allocator on the stream the call runs on, so a call may be captured into a CUDA graph, and
+calls on different streams share nothing.  Inputs (an EmbedOrder among them) that were made on
+another stream than the call's are the caller's to order and to keep, as with any torch operation.
 """
 from __future__ import annotations
 
