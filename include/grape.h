@@ -501,11 +501,12 @@ GRAPE_API int grape_head_loss(const void* H, const void* W, const void* labels, 
  *   loss[n]    = weights[n] * temperature^2 * sum_k q[n][k] (log q[n][k] - log p[n][index k])
  *   Gout[n][v] = weights[n] * temperature * (p[n][v] - sum of q[n][k] with index k = v)
  * Gout is the gradient with respect to the logits: Gout of a head that is a layer of the stack.
- * One entry of any value is a hard label.  An index that occurs twice counts with both masses.
+ * One entry of any finite value is a hard label.  An index that occurs twice counts with both masses,
+ * and an entry whose value is -inf with none.
  *  logits     N x vocab, dtype
  *  indices    N x K token numbers, values N x K in value_dtype (1 <= K <= 1024)
- *  weights    N floats, NULL for 1.  A row with weight 0 or without a valid entry has loss 0 and
- *             Gout 0, whatever its logits hold.
+ *  weights    N floats, NULL for 1.  A row with weight 0, without a valid entry or with none but
+ *             -inf in them has loss 0 and Gout 0, whatever its logits hold.
  *  Gout       N x vocab, dtype; may be `logits` itself (overwritten in place) and must not
  *             overlap it otherwise
  * Statistics are fp32, Gout is rounded once.  If a bounded device-side wait gives up, the loss of every

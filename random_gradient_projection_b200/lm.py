@@ -233,7 +233,7 @@ def head_loss(H, W, labels, weights=None, grad: bool = True, weight_grad: bool =
 
 def distill_loss(logits, indices, values, weights=None, temperature: float = 1.0, out=None, stream=None):
     """(losses, Gout) of distillation from a teacher's top logits: ``values`` at vocabulary
-    numbers ``indices`` (..., K), a negative index for an absent entry.
+    numbers ``indices`` (..., K); an index outside the vocabulary is an absent entry.
 
     ``out`` may be ``logits`` itself: Gout then replaces them."""
     dev = torch.cuda.current_device()
