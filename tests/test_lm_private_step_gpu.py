@@ -191,7 +191,7 @@ def test_graphs_are_kept_when_the_norms_lie_elsewhere_each_step():
     run(3, lambda s: 0)
     fixed, moving = run(24, lambda s: 0), run(24, lambda s: s % 12)
     print(f"median host time of a step: fixed {fixed * 1e6:.0f} us, moving {moving * 1e6:.0f} us")
-    assert moving <= 1.7 * fixed
+    assert moving <= 3 * fixed        # (5.8 times with a capture each; room for a busy host)
     # and without the share, and with it again
     for x in (None, pool[3], None, pool[5]):
         g.set_extra_sqnorms(x)
